@@ -587,6 +587,171 @@ dc_status dc_apply_baseline_multitenant_group(const dc_baseline_view* views, int
                                               const int32_t* tenant_ids, uint16_t* const* y, int32_t T,
                                               void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * The rest of a decoder layer's step around the delta products: the paged
+ * key/value cache (append, attention) and a 4-bit backbone.  Conventions as
+ * for every call; activations are bf16.
+ *
+ * dc_kv_cache -- a pool of pages of `page` token slots.  Slot s of page p, kv
+ * head h, element d of the keys is at k + p page_stride + h head_stride +
+ * s slot_stride + d (elements), the values likewise at v: pages of
+ * [heads][page][dim] and of [page][heads][dim] are both such caches, and keys
+ * and values may share an allocation.
+ *   dtype   DC_KV_BF16; DC_KV_E4M3: one byte a value, the value being code *
+ *           scale[h] with fp32 scales per kv head (device; NULL: 1)
+ *   dim     64 or 128; page a power of two, 16 .. 1024
+ *   strides multiples of 16 bytes; no two (page, head, slot) may overlap
+ *           (heads behind slots or slots behind heads, pages behind both)
+ */
+enum { DC_KV_BF16 = 0, DC_KV_E4M3 = 1 };
+
+typedef struct dc_kv_cache {
+  int32_t dtype;
+  int32_t heads; /* kv heads */
+  int32_t dim;   /* elements of a head */
+  int32_t page;  /* token slots of a page */
+  int32_t num_pages;
+  int64_t page_stride, head_stride, slot_stride;
+  void* k; /* device */
+  void* v;
+  const float* k_scale; /* device fp32 [heads], DC_KV_E4M3 only; NULL: 1 */
+  const float* v_scale;
+} dc_kv_cache;
+
+/* The position rotation: pair i < rot/2 of a head's first `rot` elements turns
+ * by pos * inv_freq[i] radians; the pair is (i, i + rot/2), or (2i, 2i+1) when
+ * `interleaved`.  rot: a multiple of 16 up to dim. */
+typedef struct dc_rope {
+  const double* inv_freq; /* device fp64 [rot/2] */
+  int32_t rot;
+  int32_t interleaved;
+} dc_rope;
+
+/*
+ * dc_kv_append -- N new tokens: q rotated into q_out, k rotated into the
+ * cache, v into the cache, in one launch.
+ *   rope      NULL: no rotation (pos is then not read and may be NULL)
+ *   q         device bf16 [N][q_heads * dim], rows q_stride elements apart; the
+ *             same for k and v ([N][kv heads * dim]) and q_out: columns of one
+ *             fused projection are such rows.  q_heads = 0: no queries (q and
+ *             q_out are not used)
+ *   q_out     may be q itself (same pointer and stride); must not overlap k, v
+ *             or otherwise q.  Strides: multiples of 8 elements
+ *   pos       device int32 [N], any position
+ *   slots     device int64 [N]: page * tokens per page + slot; a token whose
+ *             slot is negative or past the cache is not stored (a padded row:
+ *             its q is rotated all the same).  Slots of one call must differ:
+ *             of two equal ones either token's pieces may be found there
+ * Arithmetic: the angle in fp64, its sine and cosine and the products in
+ * fp32, one rounding.  An e4m3 cache gets e4m3(x / scale), saturated at +-448
+ * (infinities too; NaN stays NaN).
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
+ * (a page's slots of one head span 1 GiB or more).  N = 0 is a no-op.
+ */
+dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_t* q, int64_t q_stride,
+                       const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* pos,
+                       const int64_t* slots, uint16_t* q_out, int64_t q_out_stride, int32_t q_heads, int32_t N,
+                       void* stream);
+
+/*
+ * dc_attn_batch -- the sequences of an attention call and the prefixes their
+ * groups share.  The arrays are device memory and are read by the kernels
+ * only, so a captured call follows them; the host gives bounds, which choose
+ * the launch.
+ *   q_start   [seqs+1] non-decreasing: sequence b's query tokens are rows
+ *             q_start[b] .. q_start[b+1]-1 of q (none is allowed)
+ *   kv_len    [seqs]: keys in its own pages, its query tokens' among them (0
+ *             is allowed)
+ *   pages     [seqs][seq_pages]: page numbers; entries past the length are not
+ *             read
+ *   group_start [groups+1] non-decreasing: sequences group_start[g] ..
+ *             group_start[g+1]-1 share prefix g (none is allowed; sequences
+ *             outside every group have no prefix)
+ *   prefix_len [groups], prefix_pages [groups][prefix_pages_per_group]
+ *   max_*     at least the largest number of query tokens of a sequence, of
+ *             own keys, of query tokens of a group, of prefix keys
+ * Query token j of the n of sequence b sees its group's whole prefix and the
+ * own keys 0 .. kv_len[b] - n + j.
+ */
+typedef struct dc_attn_batch {
+  int32_t seqs, max_q, max_kv, seq_pages;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* pages;
+  int32_t groups, max_group_q, max_prefix, prefix_pages_per_group;
+  const int32_t* group_start;
+  const int32_t* prefix_len;
+  const int32_t* prefix_pages;
+} dc_attn_batch;
+
+/*
+ * dc_attention -- y = sum_k softmax_k(scale q.k) v_k over the keys each query
+ * sees; query head h reads kv head h / (q_heads / kv heads).  A shared prefix
+ * is read once for its group's rows.
+ *   q, y      device bf16 [N][q_heads * dim], rows q_stride / y_stride apart
+ *             (multiples of 8 elements); must not overlap.  Rows behind the
+ *             last sequence are left as they are
+ *   scale     finite, > 0
+ *   ws        ws_bytes >= dc_attention_workspace_bytes(kv, b, q_heads, N)
+ * A row that sees no key gets zeros.  What lies in slots that a row does not
+ * see (infinities and NaN included) does not reach it.
+ * Arithmetic: bf16 products with fp32 sums; the weights enter the second
+ * product as bf16 (as two bf16 pieces where at most 16 rows share the keys),
+ * and the row's sum is taken of the weights as they entered; joined in a fixed
+ * order, so repeated calls give the same bits; one rounding at the end.
+ * Contract violations never reach outside the buffers: lengths are cut to the
+ * bounds, rows to N, and page numbers outside the cache read page 0; what is
+ * written for such sequences is unspecified.
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE (a page table too narrow for its
+ * bound, q_heads no multiple of the kv heads), DC_ERR_ALIGN, DC_ERR_BUFFER,
+ * DC_ERR_UNSUPPORTED (2^31 query rows or launched blocks).
+ */
+size_t dc_attention_workspace_bytes(const dc_kv_cache* kv, const dc_attn_batch* b, int32_t q_heads, int32_t N);
+dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint16_t* q, int64_t q_stride,
+                       int32_t q_heads, float scale, uint16_t* y, int64_t y_stride, int32_t N, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * A backbone matrix at 4 bits with the storage and the quantizer of the
+ * deltas: groups of 128 consecutive inputs of a row, fp16 scale s and fp16
+ * integer zero z, W[o][k] = s (q - z).
+ * Format: codes as uint32 words [out/16][in/128][4][16][4]: word (T, g, c, i, j)
+ * holds row 16T+i, columns 128g + 32c + 8j + e (e < 8), code e at bit
+ * 4(e/2) + 16(e%2), so that word >> 4p & 0x000F000F holds codes 2p and 2p+1 in
+ * its halves and the 16-byte pieces of a 16-row tile are the lanes of a
+ * matrix-core operand; then uint32 [in/128][out]: s | z << 16.
+ * out and in: positive multiples of 128.
+ */
+typedef struct dc_w4_view {
+  int32_t out, in;
+  const void* base; /* device pointer to dc_w4_bytes(out, in) bytes, 16-byte aligned */
+} dc_w4_view;
+
+/* Size in bytes of the format; 0 if the shape is invalid. */
+size_t dc_w4_bytes(int32_t out, int32_t in);
+
+/*
+ * dc_w4_pack_device -- quantize a bf16 matrix [out][in] into the 4-bit format
+ * on the GPU (the quantizer of dc_pack at 4 bits).  flag: device uint32, set
+ * to 0 by the call and to 1 if an entry is not finite or a scale overflows
+ * fp16 (those groups are unspecified).  Errors: DC_ERR_INVALID_ARG,
+ * DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_BUFFER, DC_ERR_UNSUPPORTED (2^31 entries).
+ */
+dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* dst, size_t dst_bytes, uint32_t* flag,
+                            void* stream);
+
+/*
+ * dc_apply_w4 -- y = W x for T tokens (meant for few; any number is served).
+ *   x  device bf16 [T][in], y  device bf16 [T][out], fully overwritten, rounded
+ *      once from fp32 sums in a fixed order; must not overlap
+ * The codes are multiplied as 128 + q and the 128 + z taken off the group's sum
+ * (relative to the group's sum of |x| this costs 2^-17); a token with
+ * an entry that is not finite, or of 2^119 or more, may get NaN throughout.
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
+ * (2^31 entries, or more than 1048560 tokens).
+ */
+dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32_t T, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,4 +14,6 @@ from ._lib import (  # noqa: F401
     dc_apply_baseline_multitenant_group, dc_baseline_algorithmic_bytes, dc_baseline_bytes,
     dc_baseline_workspace_bytes, dc_pack_bitdelta, dc_pack_lowrank,
     DC_ERR_MAX_WIDTHS, dc_error_table, dc_error_table_workspace_bytes, dc_svd, dc_svd_workspace_bytes,
+    DC_KV_BF16, DC_KV_E4M3, AttnBatch, KvCache, Rope, W4View, dc_apply_w4, dc_attention, dc_attention_workspace_bytes,
+    dc_kv_append, dc_w4_bytes, dc_w4_pack_device,
 )

@@ -37,12 +37,16 @@ EXPORTS = ("dc_status_string", "dc_check_spec", "dc_packed_bytes", "dc_algorithm
            "dc_apply_multitenant_group_timed", "dc_baseline_bytes", "dc_baseline_algorithmic_bytes",
            "dc_pack_lowrank", "dc_pack_bitdelta", "dc_baseline_workspace_bytes",
            "dc_apply_baseline_multitenant", "dc_apply_baseline_multitenant_group",
-           "dc_error_table_workspace_bytes", "dc_error_table", "dc_svd_workspace_bytes", "dc_svd")
+           "dc_error_table_workspace_bytes", "dc_error_table", "dc_svd_workspace_bytes", "dc_svd",
+           "dc_kv_append", "dc_attention_workspace_bytes", "dc_attention", "dc_w4_bytes", "dc_w4_pack_device",
+           "dc_apply_w4")
 DC_ERR_MAX_WIDTHS = 8
 DC_KIND_LOWRANK, DC_KIND_BITDELTA = 1, 2
+DC_KV_BF16, DC_KV_E4M3 = 0, 1
 _SIZE_FNS = ("dc_status_string", "dc_packed_bytes", "dc_algorithmic_bytes", "dc_workspace_bytes",
              "dc_group_workspace_bytes", "dc_baseline_bytes", "dc_baseline_algorithmic_bytes",
-             "dc_baseline_workspace_bytes", "dc_error_table_workspace_bytes", "dc_svd_workspace_bytes")
+             "dc_baseline_workspace_bytes", "dc_error_table_workspace_bytes", "dc_svd_workspace_bytes",
+             "dc_attention_workspace_bytes", "dc_w4_bytes")
 STAGES = ("route", "xprep", "base", "vside", "uside")
 
 
@@ -64,6 +68,29 @@ class dc_delta_view(ctypes.Structure):
 class dc_baseline_view(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("out", ctypes.c_int32), ("in_", ctypes.c_int32),
                 ("r", ctypes.c_int32), ("base", ctypes.c_void_p)]
+
+
+class dc_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class dc_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class dc_attn_batch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("seq_pages", ctypes.c_int32), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("groups", ctypes.c_int32), ("max_group_q", ctypes.c_int32),
+                ("max_prefix", ctypes.c_int32), ("prefix_pages_per_group", ctypes.c_int32),
+                ("group_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("prefix_pages", ctypes.c_void_p)]
+
+
+class dc_w4_view(ctypes.Structure):
+    _fields_ = [("out", ctypes.c_int32), ("in_", ctypes.c_int32), ("base", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -133,6 +160,16 @@ def lib() -> ctypes.CDLL:
         L.dc_svd_workspace_bytes.restype = ctypes.c_size_t
         L.dc_svd_workspace_bytes.argtypes = [i32, i32]
         L.dc_svd.argtypes = [i32, i32, i32, _P, _P, _P, _P, _P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), _P]
+        i64 = ctypes.c_int64
+        kp, ap = ctypes.POINTER(dc_kv_cache), ctypes.POINTER(dc_attn_batch)
+        L.dc_kv_append.argtypes = [kp, ctypes.POINTER(dc_rope), _P, i64, _P, i64, _P, i64, _P, _P, _P, i64, i32, i32, _P]
+        L.dc_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.dc_attention_workspace_bytes.argtypes = [kp, ap, i32, i32]
+        L.dc_attention.argtypes = [kp, ap, _P, i64, i32, ctypes.c_float, _P, i64, i32, _P, ctypes.c_size_t, _P]
+        L.dc_w4_bytes.restype = ctypes.c_size_t
+        L.dc_w4_bytes.argtypes = [i32, i32]
+        L.dc_w4_pack_device.argtypes = [i32, i32, _P, _P, ctypes.c_size_t, _P, _P]
+        L.dc_apply_w4.argtypes = [ctypes.POINTER(dc_w4_view), _P, _P, i32, _P]
         for name in EXPORTS:
             if name not in _SIZE_FNS:
                 getattr(L, name).restype = ctypes.c_int32
@@ -539,3 +576,199 @@ def dc_svd(delta, r: int, U, sigma, V, ws, stream=None) -> int:
                         _dptr(V, "V"), _dptr(ws, "ws"), ws.numel() * ws.element_size(), ctypes.byref(sw),
                         _stream(stream)), "dc_svd")
     return int(sw.value)
+
+
+# ------------------------------------------- decoder layer: cache, attention
+# These calls take tensors of any row stride, so the binding checks what the
+# library cannot see: element types, shapes, that every tensor is on one
+# device and that this device is the current one (its stream is used).
+def _typed(t, what: str, names, contiguous: bool = True):
+    if str(t.dtype)[6:] not in names:   # "torch.xxx"
+        raise ValueError("%s must be %s, not %s" % (what, " or ".join(names), t.dtype))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+    return t
+
+
+_BF16 = ("bfloat16", "int16", "uint16")   # bf16 tensors, or their bits
+
+
+def _current(device: int, stream) -> int:
+    """The stream of a call on tensors of `device`, which must be current."""
+    import torch
+    if torch.cuda.current_device() != device:
+        raise ValueError("the tensors are on device %d, the current one is %d" % (device, torch.cuda.current_device()))
+    return int(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+
+
+def _same_device(device: int, **ts) -> None:
+    for what, t in ts.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError("%s is not on device %d" % (what, device))
+
+
+class KvCache:
+    """A paged key/value cache in device memory (keeps its tensors alive): k
+    and v [pages][heads][page][dim] of bf16 or e4m3, with any strides that
+    keep dim contiguous (a [pages][page][heads][dim] pool is its transposed
+    view) and the same ones for both; k_scale and v_scale fp32 [heads] for
+    e4m3 caches, None: 1."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        e4m3 = ("float8_e4m3fn", "uint8")
+        _typed(k, "k", _BF16 + e4m3, False)
+        if v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride() or k.dim() != 4:
+            raise ValueError("k and v must be [pages][heads][page][dim] of one type, shape and stride")
+        if k.stride(3) != 1:
+            raise ValueError("the elements of a head must be contiguous")
+        self.device = k.get_device()
+        _same_device(self.device, v=v, k_scale=k_scale, v_scale=v_scale)
+        for s, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if s is not None and _typed(s, what, ("float32",)).numel() != k.shape[1]:
+                raise ValueError("%s must have one value a head" % what)
+        self._keep = (k, v, k_scale, v_scale)
+        pages, self.heads, page, self.dim = k.shape
+        ptr = lambda t: None if t is None else int(t.data_ptr())  # noqa: E731
+        ps, hs, ss, _ = k.stride()
+        # the stride of an axis of one entry is any number: give it what a packed cache has
+        ss = max(ss, self.dim) if page > 1 else self.dim
+        hs = hs if self.heads > 1 else max(ss * page, self.dim)
+        ps = ps if pages > 1 else max(hs * self.heads, ss * page)
+        self.c = dc_kv_cache(DC_KV_E4M3 if k.element_size() == 1 else DC_KV_BF16, self.heads, self.dim, page, pages, ps,
+                             hs, ss, ptr(k), ptr(v), ptr(k_scale), ptr(v_scale))
+        self.ref = ctypes.byref(self.c)
+
+
+class Rope:
+    """The position rotation: inv_freq fp64 [rot/2] (device)."""
+
+    def __init__(self, inv_freq, interleaved: bool = False):
+        self._keep = _typed(inv_freq, "inv_freq", ("float64",))
+        self.device = inv_freq.get_device()
+        self.c = dc_rope(int(inv_freq.data_ptr()), 2 * inv_freq.numel(), int(bool(interleaved)))
+        self.ref = ctypes.byref(self.c)
+
+
+def _rows(t, what: str, n: int, cols: int) -> int:
+    """The row stride of bf16 rows [n][cols] (heads side by side)."""
+    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be [%d][%d] with contiguous rows" % (what, n, cols))
+    if str(t.dtype)[6:] not in _BF16:
+        raise ValueError("%s must be bf16" % what)
+    return t.stride(0) if n > 1 else cols
+
+
+def dc_kv_append(cache: KvCache, q, k, v, pos, slots, rope: Rope, q_out, stream=None) -> None:
+    """N new tokens: q rotated into q_out (q itself is allowed), k rotated and
+    v into the cache at slots.  q, q_out [N][q_heads*dim], k, v
+    [N][heads*dim] bf16 rows of any stride; q = q_out = None: no queries.  pos
+    int32 [N], slots int64 [N]; rope None: no rotation (pos may be None)."""
+    n = k.shape[0]
+    kc = cache.heads * cache.dim
+    ks, vs = _rows(k, "k", n, kc), _rows(v, "v", n, kc)
+    _same_device(cache.device, q=q, k=k, v=v, pos=pos, slots=slots, q_out=q_out)
+    if rope is not None and (rope.device != cache.device or pos is None):
+        raise ValueError("the rotation needs pos and its frequencies on the cache's device")
+    if _typed(slots, "slots", ("int64",)).numel() != n or (
+            pos is not None and _typed(pos, "pos", ("int32",)).numel() != n):
+        raise ValueError("slots and pos must have one entry a token")
+    hq = qs = qos = 0
+    if q is not None:
+        hq = q.shape[1] // cache.dim
+        qs, qos = _rows(q, "q", n, hq * cache.dim), _rows(q_out, "q_out", n, hq * cache.dim)
+    _check(lib().dc_kv_append(cache.ref, rope.ref if rope is not None else None,
+                              q.data_ptr() if hq else None, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                              pos.data_ptr() if pos is not None else None, slots.data_ptr(),
+                              q_out.data_ptr() if hq else None, qos, hq, n, _current(cache.device, stream)),
+           "dc_kv_append")
+
+
+class AttnBatch:
+    """The sequences of an attention call and the prefixes that their groups
+    share (keeps its tensors alive; see dc_attn_batch): q_start int32 [B+1],
+    kv_len int32 [B], pages int32 [B][width]; group_start int32 [G+1],
+    prefix_len int32 [G], prefix_pages int32 [G][width].  The contents may
+    change between calls as long as the bounds hold."""
+
+    def __init__(self, q_start, kv_len, pages, max_q: int, max_kv: int, group_start=None, prefix_len=None,
+                 prefix_pages=None, max_prefix: int = 0, max_group_q: int = 0):
+        i32 = ("int32",)
+        b = kv_len.numel()
+        if _typed(q_start, "q_start", i32).numel() != b + 1 or _typed(kv_len, "kv_len", i32).dim() != 1 or \
+                _typed(pages, "pages", i32).dim() != 2 or pages.shape[0] < b:
+            raise ValueError("q_start must be [B+1], kv_len [B] and pages [B][width]")
+        self.device = kv_len.get_device()
+        g = gw = 0
+        ptrs = (None, None, None)
+        if group_start is not None:
+            g = prefix_len.numel()
+            if _typed(group_start, "group_start", i32).numel() != g + 1 or \
+                    _typed(prefix_len, "prefix_len", i32).dim() != 1 or \
+                    _typed(prefix_pages, "prefix_pages", i32).dim() != 2 or prefix_pages.shape[0] < g:
+                raise ValueError("group_start must be [G+1], prefix_len [G] and prefix_pages [G][width]")
+            gw = prefix_pages.shape[1]
+            ptrs = tuple(int(t.data_ptr()) for t in (group_start, prefix_len, prefix_pages))
+        _same_device(self.device, q_start=q_start, pages=pages, group_start=group_start, prefix_len=prefix_len,
+                     prefix_pages=prefix_pages)
+        self._keep = (q_start, kv_len, pages, group_start, prefix_len, prefix_pages)
+        self.c = dc_attn_batch(b, int(max_q), int(max_kv), pages.shape[1], int(q_start.data_ptr()),
+                               int(kv_len.data_ptr()), int(pages.data_ptr()), g, int(max_group_q), int(max_prefix), gw,
+                               *ptrs)
+        self.ref = ctypes.byref(self.c)
+
+
+def dc_attention_workspace_bytes(cache: KvCache, batch: AttnBatch, q_heads: int, n: int) -> int:
+    return int(lib().dc_attention_workspace_bytes(cache.ref, batch.ref, int(q_heads), int(n)))
+
+
+def dc_attention(cache: KvCache, q, batch: AttnBatch, scale: float, y, ws, stream=None) -> None:
+    """y = softmax(scale q k) v over the cache: q and y [N][q_heads*dim] bf16
+    rows of any stride."""
+    n, cols = q.shape
+    hq = cols // cache.dim
+    qs, ys = _rows(q, "q", n, hq * cache.dim), _rows(y, "y", n, hq * cache.dim)
+    if batch.device != cache.device:
+        raise ValueError("the batch and the cache are on different devices")
+    _same_device(cache.device, q=q, y=y, ws=ws)
+    _check(lib().dc_attention(cache.ref, batch.ref, q.data_ptr(), qs, hq, scale, y.data_ptr(), ys, n, _dptr(ws, "ws"),
+                              ws.numel() * ws.element_size(), _current(cache.device, stream)), "dc_attention")
+
+
+# ---------------------------------------------------------- 4-bit backbone
+def dc_w4_bytes(out: int, inn: int) -> int:
+    return int(lib().dc_w4_bytes(int(out), int(inn)))
+
+
+class W4View:
+    """A backbone matrix in the 4-bit format (keeps its tensor alive)."""
+
+    def __init__(self, out: int, inn: int, buf):
+        need = dc_w4_bytes(out, inn)
+        if not buf.is_contiguous() or buf.numel() * buf.element_size() < need:
+            raise ValueError("the buffer must be contiguous and hold %d bytes" % need)
+        self.out, self.inn, self.buf, self.device = int(out), int(inn), buf, buf.get_device()
+        self.c = dc_w4_view(self.out, self.inn, int(buf.data_ptr()))
+        self.ref = ctypes.byref(self.c)
+
+
+def dc_w4_pack_device(W, dst, flag, stream=None) -> None:
+    """Quantize W (bf16 [out][in], device) into the 4-bit format: dst of
+    dc_w4_bytes(out, in) bytes, flag int32/uint32 [1]."""
+    out, inn = W.shape
+    _typed(W, "W", _BF16)
+    _typed(flag, "flag", ("int32", "uint32"))
+    _same_device(W.get_device(), dst=dst, flag=flag)
+    _check(lib().dc_w4_pack_device(int(out), int(inn), _dptr(W, "W"), _dptr(dst, "dst"),
+                                   dst.numel() * dst.element_size(), _dptr(flag, "flag"),
+                                   _current(W.get_device(), stream)), "dc_w4_pack_device")
+
+
+def dc_apply_w4(view: W4View, x, y, stream=None) -> None:
+    """y [T][out] = W x, x [T][in], both bf16 and contiguous."""
+    t = x.shape[0]
+    if x.dim() != 2 or x.shape[1] != view.inn or y.shape != (t, view.out):
+        raise ValueError("x must be [T][%d] and y [T][%d]" % (view.inn, view.out))
+    _typed(x, "x", _BF16)
+    _typed(y, "y", _BF16)
+    _same_device(view.device, x=x, y=y)
+    _check(lib().dc_apply_w4(view.ref, x.data_ptr(), y.data_ptr(), t, _current(view.device, stream)), "dc_apply_w4")

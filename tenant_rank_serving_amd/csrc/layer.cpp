@@ -1,0 +1,293 @@
+// Entry points of the decoder-layer operators (paged key/value cache, 4-bit
+// backbone): argument checks on the host, then one launcher.  No allocation,
+// no synchronization.
+#include <cmath>
+#include <cstdint>
+
+#include "layer.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Rows of `w` bytes, `n` of them `stride` bytes apart: whether two such
+// buffers share a byte.  Buffers of one stride may be interleaved (columns of
+// one fused matrix); of other pairs whose ranges meet nothing is known, so
+// they count as sharing.
+bool rows_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb, int64_t wb, int64_t n) {
+  if (n <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t xe = x + (uintptr_t)((n - 1) * sa + wa), ye = y + (uintptr_t)((n - 1) * sb + wb);
+  if (xe <= y || ye <= x) return false;
+  if (n == 1 || sa != sb) return true;
+  const int64_t d = (int64_t)((y >= x ? y - x : x - y) % (uintptr_t)sa);
+  const int64_t u = y >= x ? wa : wb, v = y >= x ? wb : wa;   // the lower buffer's rows, the upper one's
+  return d < u || d + v > sa;
+}
+
+bool mul_fits(int64_t a, int64_t b, int64_t lim) { return a == 0 || b <= lim / a; }
+
+// The cache's shape and strides; fills the kernels' view of it.
+dc_status check_cache(const dc_kv_cache* c, dc::KvArgs* k) {
+  if (!c) return DC_ERR_INVALID_ARG;
+  if (c->dtype != DC_KV_BF16 && c->dtype != DC_KV_E4M3) return DC_ERR_INVALID_ARG;
+  if (c->heads < 1 || (c->dim != 64 && c->dim != 128) || c->num_pages < 1) return DC_ERR_SHAPE;
+  if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1))) return DC_ERR_SHAPE;
+  if (!c->k || !c->v) return DC_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return DC_ERR_ALIGN;
+  const int64_t e = c->dtype == DC_KV_BF16 ? 2 : 1;
+  if (c->dtype == DC_KV_BF16 && (c->k_scale || c->v_scale)) return DC_ERR_INVALID_ARG;
+  const int64_t lim = INT64_C(1) << 62;
+  if (c->slot_stride < c->dim || c->head_stride < c->dim || c->page_stride < c->dim) return DC_ERR_SHAPE;
+  if ((c->slot_stride * e) % 16 || (c->head_stride * e) % 16 || (c->page_stride * e) % 16) return DC_ERR_ALIGN;
+  // no two rows share an element: heads behind slots or slots behind heads, pages behind both
+  if (!mul_fits(c->page, c->slot_stride, lim / 4) || !mul_fits(c->heads, c->head_stride, lim / 4) ||
+      !mul_fits(c->num_pages, c->page_stride, lim / 4))
+    return DC_ERR_UNSUPPORTED;
+  const int64_t slots = (c->page - 1) * c->slot_stride + c->dim, heads = (c->heads - 1) * c->head_stride + c->dim;
+  if (!(c->heads == 1 || c->head_stride >= slots || c->slot_stride >= heads)) return DC_ERR_SHAPE;
+  if (c->num_pages > 1 && c->page_stride < (c->page - 1) * c->slot_stride + (c->heads - 1) * c->head_stride + c->dim)
+    return DC_ERR_SHAPE;
+  if (slots * e > INT32_MAX / 2) return DC_ERR_UNSUPPORTED;   // 32-bit offsets inside a page
+  k->k = static_cast<uint8_t*>(c->k);
+  k->v = static_cast<uint8_t*>(c->v);
+  k->ks = c->k_scale;
+  k->vs = c->v_scale;
+  k->page_stride = c->page_stride * e;
+  k->head_stride = c->head_stride * e;
+  k->slot_stride = c->slot_stride * e;
+  k->heads = c->heads;
+  k->num_pages = c->num_pages;
+  k->shift = 0;
+  while ((1 << k->shift) < c->page) ++k->shift;
+  return DC_OK;
+}
+
+// A row-strided bf16 matrix [n][cols].
+dc_status check_rows(const void* p, int64_t stride, int64_t cols) {
+  if (!p) return DC_ERR_INVALID_ARG;
+  if (stride < cols || stride > (INT64_C(1) << 40)) return DC_ERR_SHAPE;
+  if (!aligned(p, 16) || stride % 8) return DC_ERR_ALIGN;
+  return DC_OK;
+}
+
+dc_status check_batch(const dc_kv_cache* kv, const dc_attn_batch* b, int32_t q_heads, int32_t N) {
+  if (!b || N < 0 || q_heads < 1) return DC_ERR_INVALID_ARG;
+  if (q_heads % kv->heads) return DC_ERR_SHAPE;
+  if (b->seqs < 0 || b->max_q < 0 || b->max_kv < 0 || b->groups < 0 || b->max_group_q < 0 || b->max_prefix < 0)
+    return DC_ERR_INVALID_ARG;
+  if (b->seq_pages < 0 || b->prefix_pages_per_group < 0) return DC_ERR_INVALID_ARG;
+  if ((int64_t)b->seq_pages * kv->page < b->max_kv) return DC_ERR_SHAPE;
+  if (b->groups > 0 && (int64_t)b->prefix_pages_per_group * kv->page < b->max_prefix) return DC_ERR_SHAPE;
+  // the kernels number query rows and keys with 32 bits
+  if ((int64_t)N * q_heads > INT32_MAX || (int64_t)b->max_q * q_heads > INT32_MAX / 2 ||
+      (int64_t)b->max_group_q * q_heads > INT32_MAX / 2 || b->max_kv > INT32_MAX / 2 || b->max_prefix > INT32_MAX / 2)
+    return DC_ERR_UNSUPPORTED;
+  return DC_OK;
+}
+
+// Blocks of either form, at most (64 bits: the launch needs 32).
+int64_t blocks_of(const dc::AttnPlan& p, int64_t B, int64_t G, int64_t heads) {
+  if (p.rows) return (B * heads + 7) / 8 * 8 * p.rbo;
+  return B * heads * p.rbo * p.so + G * heads * p.rbp * p.sp;
+}
+
+}  // namespace
+
+namespace dc {
+
+AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, int32_t max_q, int32_t max_kv, int32_t G,
+                   int32_t max_gq, int32_t max_pre) {
+  AttnPlan p{};
+  const int64_t ro = (int64_t)max_q * gq, rg = (int64_t)max_gq * gq;   // query rows of a sequence, of a group
+  if (max_pre == 0 || max_gq == 0) G = 0;
+  // long queries: enough blocks of 256 rows for half the card
+  const int64_t rb = (ro + 255) / 256;
+  if (ro >= 64 && (int64_t)B * hkv * rb >= 128) {
+    p.rows = true;
+    p.rbo = (int32_t)rb;
+    p.co = p.cp = 32;
+    p.direct = true;
+    return p;
+  }
+  p.ro = ro <= 16 ? 1 : 2;
+  p.rp = p.ro == 2 ? 2 : (rg <= 16 ? 1 : (rg <= 32 ? 2 : 4));
+  p.rbo = (int32_t)((ro + 16 * p.ro - 1) / (16 * p.ro));
+  p.rbp = (int32_t)((rg + 16 * p.rp - 1) / (16 * p.rp));
+  // as many ranges as fill the card twice, each of 128 keys (a step a wave) or more
+  auto split = [](int64_t items, int64_t keys, int64_t want, int32_t* s, int32_t* c) {
+    if (items < 1) items = 1;
+    int64_t n = (want + items - 1) / items;
+    const int64_t most = (keys + 127) / 128;
+    if (n > most) n = most;
+    if (n > 64) n = 64;
+    if (n < 1) n = 1;
+    int64_t ch = ((keys + n - 1) / n + 31) / 32 * 32;
+    if (ch < 32) ch = 32;
+    *c = (int32_t)ch;
+    *s = (int32_t)((keys + ch - 1) / ch);
+  };
+  split((int64_t)B * hkv * p.rbo, max_kv, 512, &p.so, &p.co);
+  p.cp = 32;
+  if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, p.rp == 4 ? 256 : 512, &p.sp, &p.cp);
+  if (p.sp == 0 && p.so <= 1) {
+    p.so = 1;
+    p.direct = true;
+    return p;
+  }
+  const size_t rows = (size_t)n * hkv * gq, slots = (size_t)p.sp + p.so;
+  p.o_off = round_up(8 * rows * slots, kAlign);
+  p.ws = round_up(p.o_off + 4 * rows * slots * dim, kAlign);
+  return p;
+}
+
+}  // namespace dc
+
+extern "C" {
+
+dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_t* q, int64_t q_stride,
+                       const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* pos,
+                       const int64_t* slots, uint16_t* q_out, int64_t q_out_stride, int32_t q_heads, int32_t N,
+                       void* stream) {
+  dc::AppendArgs a{};
+  dc_status st = check_cache(kv, &a.kv);
+  if (st != DC_OK) return st;
+  if (N < 0 || q_heads < 0) return DC_ERR_INVALID_ARG;
+  const int64_t qc = (int64_t)q_heads * kv->dim, kc = (int64_t)kv->heads * kv->dim;
+  if ((qc + 2 * kc) / 16 > INT32_MAX / 2) return DC_ERR_UNSUPPORTED;
+  if (rope) {
+    if (rope->rot < 16 || rope->rot > kv->dim || rope->rot % 16) return DC_ERR_SHAPE;
+    if (!rope->inv_freq || !pos) return DC_ERR_INVALID_ARG;
+    if (!aligned(rope->inv_freq, 8) || !aligned(pos, 4)) return DC_ERR_ALIGN;
+  }
+  if (q_heads > 0) {
+    if ((st = check_rows(q, q_stride, qc)) != DC_OK) return st;
+    if ((st = check_rows(q_out, q_out_stride, qc)) != DC_OK) return st;
+    const bool in_place = q == q_out && q_stride == q_out_stride;
+    if (!in_place && rows_meet(q, 2 * q_stride, 2 * qc, q_out, 2 * q_out_stride, 2 * qc, N)) return DC_ERR_INVALID_ARG;
+  }
+  if ((st = check_rows(k, k_stride, kc)) != DC_OK) return st;
+  if ((st = check_rows(v, v_stride, kc)) != DC_OK) return st;
+  if (q_heads > 0 && (rows_meet(k, 2 * k_stride, 2 * kc, q_out, 2 * q_out_stride, 2 * qc, N) ||
+                      rows_meet(v, 2 * v_stride, 2 * kc, q_out, 2 * q_out_stride, 2 * qc, N)))
+    return DC_ERR_INVALID_ARG;
+  if (!slots) return DC_ERR_INVALID_ARG;
+  if (!aligned(slots, 8)) return DC_ERR_ALIGN;
+  if (N == 0) return DC_OK;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qs = q_stride;
+  a.ks = k_stride;
+  a.vs = v_stride;
+  a.qos = q_out_stride;
+  a.pos = pos;
+  a.slots = slots;
+  a.freq = rope ? rope->inv_freq : nullptr;
+  a.qo = q_out;
+  a.hq = q_heads;
+  a.dim = kv->dim;
+  a.rot = rope ? rope->rot : 0;
+  a.interleaved = rope ? rope->interleaved != 0 : 0;
+  a.e4m3 = kv->dtype == DC_KV_E4M3;
+  a.n = N;
+  a.stream = stream;
+  return dc::launch_append(a) == 0 ? DC_OK : DC_ERR_HIP;
+}
+
+size_t dc_attention_workspace_bytes(const dc_kv_cache* kv, const dc_attn_batch* b, int32_t q_heads, int32_t N) {
+  dc::KvArgs k{};
+  if (check_cache(kv, &k) != DC_OK || check_batch(kv, b, q_heads, N) != DC_OK) return 0;
+  const dc::AttnPlan p = dc::attn_plan(kv->heads, q_heads / kv->heads, kv->dim, N, b->seqs, b->max_q, b->max_kv,
+                                       b->groups, b->max_group_q, b->max_prefix);
+  return p.ws > 0 ? p.ws : dc::kAlign;
+}
+
+dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint16_t* q, int64_t q_stride,
+                       int32_t q_heads, float scale, uint16_t* y, int64_t y_stride, int32_t N, void* ws,
+                       size_t ws_bytes, void* stream) {
+  dc::AttnArgs a{};
+  dc_status st = check_cache(kv, &a.kv);
+  if (st != DC_OK) return st;
+  if ((st = check_batch(kv, b, q_heads, N)) != DC_OK) return st;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return DC_ERR_INVALID_ARG;
+  const int64_t qc = (int64_t)q_heads * kv->dim;
+  if ((st = check_rows(q, q_stride, qc)) != DC_OK) return st;
+  if ((st = check_rows(y, y_stride, qc)) != DC_OK) return st;
+  if (rows_meet(q, 2 * q_stride, 2 * qc, y, 2 * y_stride, 2 * qc, N)) return DC_ERR_INVALID_ARG;
+  if (!ws) return DC_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return DC_ERR_ALIGN;
+  if (b->seqs > 0) {
+    if (!b->q_start || !b->kv_len || (b->max_kv > 0 && !b->pages)) return DC_ERR_INVALID_ARG;
+    if (!aligned(b->q_start, 4) || !aligned(b->kv_len, 4) || !aligned(b->pages, 4)) return DC_ERR_ALIGN;
+  }
+  if (b->groups > 0) {
+    if (!b->group_start || !b->prefix_len || (b->max_prefix > 0 && !b->prefix_pages)) return DC_ERR_INVALID_ARG;
+    if (!aligned(b->group_start, 4) || !aligned(b->prefix_len, 4) || !aligned(b->prefix_pages, 4)) return DC_ERR_ALIGN;
+  }
+  a.plan = dc::attn_plan(kv->heads, q_heads / kv->heads, kv->dim, N, b->seqs, b->max_q, b->max_kv, b->groups,
+                         b->max_group_q, b->max_prefix);
+  if (ws_bytes < a.plan.ws) return DC_ERR_BUFFER;
+  if (blocks_of(a.plan, b->seqs, b->groups, kv->heads) > INT32_MAX) return DC_ERR_UNSUPPORTED;
+  if (N == 0 || b->seqs == 0 || b->max_q == 0) return DC_OK;   // no query: nothing to write
+  a.q = q;
+  a.y = y;
+  a.qs = q_stride;
+  a.ys = y_stride;
+  a.scale = (float)((double)scale * 1.4426950408889634074);   // the kernels' exponentials are base 2
+  a.hq = q_heads;
+  a.gq = q_heads / kv->heads;
+  a.n = N;
+  a.dim = kv->dim;
+  a.e4m3 = kv->dtype == DC_KV_E4M3;
+  a.B = b->seqs;
+  a.max_q = b->max_q;
+  a.max_kv = b->max_kv;
+  a.pw = b->seq_pages;
+  a.q_start = b->q_start;
+  a.kv_len = b->kv_len;
+  a.pages = b->pages;
+  const bool pre = b->groups > 0 && b->max_prefix > 0 && b->max_group_q > 0;
+  a.G = pre ? b->groups : 0;
+  a.max_gq = b->max_group_q;
+  a.max_pre = b->max_prefix;
+  a.ppw = b->prefix_pages_per_group;
+  a.g_start = b->group_start;
+  a.p_len = b->prefix_len;
+  a.p_pages = b->prefix_pages;
+  a.pml = static_cast<float*>(ws);
+  a.po = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + a.plan.o_off);
+  a.stream = stream;
+  return dc::launch_attention(a) == 0 ? DC_OK : DC_ERR_HIP;
+}
+
+size_t dc_w4_bytes(int32_t out, int32_t in) {
+  if (out <= 0 || in <= 0 || out % dc::kGroup || in % dc::kGroup) return 0;
+  return (size_t)out * in / 2 + 4 * (size_t)out * (in / dc::kGroup);
+}
+
+dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* dst, size_t dst_bytes, uint32_t* flag,
+                            void* stream) {
+  const size_t need = dc_w4_bytes(out, in);
+  if (need == 0) return DC_ERR_SHAPE;
+  if (!W || !dst || !flag) return DC_ERR_INVALID_ARG;
+  if (!aligned(W, 16) || !aligned(dst, 16) || !aligned(flag, 4)) return DC_ERR_ALIGN;
+  if (dst_bytes < need) return DC_ERR_BUFFER;
+  if ((size_t)out * in > (size_t)INT32_MAX) return DC_ERR_UNSUPPORTED;
+  return dc::launch_w4_pack(out, in, W, static_cast<uint8_t*>(dst), flag, stream) == 0 ? DC_OK : DC_ERR_HIP;
+}
+
+dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32_t T, void* stream) {
+  if (!w || T < 0) return DC_ERR_INVALID_ARG;
+  if (dc_w4_bytes(w->out, w->in) == 0) return DC_ERR_SHAPE;
+  if (!w->base || !x || !y) return DC_ERR_INVALID_ARG;
+  if (!aligned(w->base, 16) || !aligned(x, 16) || !aligned(y, 16)) return DC_ERR_ALIGN;
+  if (rows_meet(x, 2 * (int64_t)w->in, 2 * (int64_t)w->in, y, 2 * (int64_t)w->out, 2 * (int64_t)w->out, T))
+    return DC_ERR_INVALID_ARG;
+  if ((size_t)w->out * w->in > (size_t)INT32_MAX || T > 65535 * 16) return DC_ERR_UNSUPPORTED;
+  if (T == 0) return DC_OK;
+  const dc::W4Args a{static_cast<const uint8_t*>(w->base), x, y, w->out, w->in, T, stream};
+  return dc::launch_w4(a) == 0 ? DC_OK : DC_ERR_HIP;
+}
+
+}  // extern "C"

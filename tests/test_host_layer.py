@@ -1,0 +1,180 @@
+"""Argument checks of the decoder-layer operators, on the CPU: device entry points are called only with arguments that
+the host refuses (or nothing to do), with made-up addresses, so no kernel is ever launched."""
+import ctypes
+import os
+
+import pytest
+
+import tenant_rank_serving_amd as trs
+from tenant_rank_serving_amd import _lib
+
+E = trs
+
+
+def cache(**kw):
+    f = dict(dtype=0, heads=4, dim=128, page=16, num_pages=10, page_stride=4 * 16 * 128, head_stride=16 * 128,
+             slot_stride=128, k=0x10000, v=0x4000000, k_scale=None, v_scale=None)
+    f.update(kw)
+    return _lib.dc_kv_cache(*(f[n] for n, _ in _lib.dc_kv_cache._fields_))
+
+
+def rope(**kw):
+    f = dict(inv_freq=0x100, rot=128, interleaved=0)
+    f.update(kw)
+    return _lib.dc_rope(*(f[n] for n, _ in _lib.dc_rope._fields_))
+
+
+def batch(**kw):
+    f = dict(seqs=2, max_q=1, max_kv=100, seq_pages=8, q_start=0x1000, kv_len=0x1100, pages=0x1200, groups=1, max_group_q=2,
+             max_prefix=50, prefix_pages_per_group=4, group_start=0x1300, prefix_len=0x1400, prefix_pages=0x1500)
+    f.update(kw)
+    return _lib.dc_attn_batch(*(f[n] for n, _ in _lib.dc_attn_batch._fields_))
+
+
+@pytest.fixture(scope="module")
+def L():
+    return trs.lib()
+
+
+def append(L, c=None, r=rope(), q=0x8000000, qs=1024, k=0x8100000, ks=512, v=0x8200000, vs=512, pos=0x200, slots=0x300,
+           qo=0x8300000, qos=1024, hq=8, n=0):
+    return L.dc_kv_append(ctypes.byref(c if c is not None else cache()), ctypes.byref(r) if r is not None else None, q, qs, k, ks,
+                          v, vs, pos, slots, qo, qos, hq, n, None)
+
+
+def test_append_with_nothing_to_do(L):
+    assert append(L) == E.DC_OK
+    assert append(L, r=None, pos=None) == E.DC_OK
+    assert append(L, hq=0, q=None, qo=None, qs=0, qos=0) == E.DC_OK
+    # pages of [slots][heads], keys and values in one allocation, e4m3 with scales
+    assert append(L, cache(slot_stride=4 * 128, head_stride=128, page_stride=2 * 4 * 16 * 128)) == E.DC_OK
+    assert append(L, cache(dtype=1, k_scale=0x40, v_scale=0x80)) == E.DC_OK
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(dtype=2), E.DC_ERR_INVALID_ARG), (dict(k=None), E.DC_ERR_INVALID_ARG), (dict(v=None), E.DC_ERR_INVALID_ARG),
+    (dict(heads=0), E.DC_ERR_SHAPE), (dict(dim=96), E.DC_ERR_SHAPE), (dict(dim=256), E.DC_ERR_SHAPE),
+    (dict(page=8), E.DC_ERR_SHAPE), (dict(page=48), E.DC_ERR_SHAPE), (dict(page=2048), E.DC_ERR_SHAPE),
+    (dict(num_pages=0), E.DC_ERR_SHAPE), (dict(k=0x10008), E.DC_ERR_ALIGN), (dict(v=0x4000001), E.DC_ERR_ALIGN),
+    (dict(slot_stride=64), E.DC_ERR_SHAPE), (dict(slot_stride=132), E.DC_ERR_ALIGN), (dict(page_stride=8196), E.DC_ERR_ALIGN),
+    (dict(head_stride=1024), E.DC_ERR_SHAPE),                    # heads that overlap
+    (dict(page_stride=4 * 16 * 128 - 128), E.DC_ERR_SHAPE),      # pages that overlap
+    (dict(k_scale=0x40), E.DC_ERR_INVALID_ARG),                  # scales of a bf16 cache
+    (dict(dtype=1, k_scale=0x42), E.DC_ERR_ALIGN),
+    (dict(dtype=1, slot_stride=136), E.DC_ERR_ALIGN),            # 16 bytes are 16 elements there
+    (dict(slot_stride=1 << 26, head_stride=128, page_stride=1 << 30), E.DC_ERR_UNSUPPORTED),
+    (dict(num_pages=1 << 30, page_stride=1 << 40), E.DC_ERR_UNSUPPORTED),
+])
+def test_cache_refusals(L, kw, want):
+    assert append(L, cache(**kw)) == want
+    b = batch()
+    assert L.dc_attention(ctypes.byref(cache(**kw)), ctypes.byref(b), 0x8000000, 1024, 8, 0.1, 0x8300000, 1024, 2, 0x100, 1 << 30,
+                          None) == want
+    assert L.dc_attention_workspace_bytes(ctypes.byref(cache(**kw)), ctypes.byref(b), 8, 2) == 0
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), E.DC_ERR_INVALID_ARG), (dict(hq=-1), E.DC_ERR_INVALID_ARG),
+    (dict(k=None), E.DC_ERR_INVALID_ARG), (dict(v=None), E.DC_ERR_INVALID_ARG), (dict(q=None), E.DC_ERR_INVALID_ARG),
+    (dict(qo=None), E.DC_ERR_INVALID_ARG), (dict(slots=None), E.DC_ERR_INVALID_ARG), (dict(pos=None), E.DC_ERR_INVALID_ARG),
+    (dict(r=rope(inv_freq=None)), E.DC_ERR_INVALID_ARG), (dict(r=rope(rot=8)), E.DC_ERR_SHAPE),
+    (dict(r=rope(rot=144)), E.DC_ERR_SHAPE), (dict(r=rope(rot=40)), E.DC_ERR_SHAPE), (dict(r=rope(inv_freq=0x104)), E.DC_ERR_ALIGN),
+    (dict(slots=0x304), E.DC_ERR_ALIGN), (dict(pos=0x202), E.DC_ERR_ALIGN), (dict(q=0x8000008), E.DC_ERR_ALIGN),
+    (dict(qs=1028), E.DC_ERR_ALIGN), (dict(qs=1016), E.DC_ERR_SHAPE), (dict(ks=0), E.DC_ERR_SHAPE), (dict(vs=504), E.DC_ERR_SHAPE),
+    # overlaps: q_out one row behind q, over k, over v; q in place with another stride
+    (dict(n=4, qo=0x8000000 + 2048), E.DC_ERR_INVALID_ARG), (dict(n=4, qo=0x8100000, qos=1024), E.DC_ERR_INVALID_ARG),
+    (dict(n=1, qo=0x8200000 - 512), E.DC_ERR_INVALID_ARG), (dict(n=2, qo=0x8000000, qos=2048), E.DC_ERR_INVALID_ARG),
+    # a fused matrix whose k columns the written q rows reach into
+    (dict(n=4, q=0x8000000, qs=2048, k=0x8000000 + 1024, ks=2048, qo=0x8000000, qos=2048), E.DC_ERR_INVALID_ARG),
+])
+def test_append_refusals(L, kw, want):
+    assert append(L, **kw) == want
+
+
+def attend(L, c=None, b=None, q=0x8000000, qs=1024, hq=8, scale=0.1, y=0x8300000, ys=1024, n=0, ws=0x100, nws=1 << 30):
+    return L.dc_attention(ctypes.byref(c or cache()), ctypes.byref(b or batch()), q, qs, hq, scale, y, ys, n, ws, nws, None)
+
+
+def test_attention_with_nothing_to_do(L):
+    assert attend(L) == E.DC_OK
+    assert attend(L, b=batch(seqs=0, q_start=None, kv_len=None, pages=None), n=5) == E.DC_OK
+    assert attend(L, b=batch(max_q=0), n=5) == E.DC_OK
+    assert attend(L, b=batch(groups=0, group_start=None, prefix_len=None, prefix_pages=None)) == E.DC_OK
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n=-1), E.DC_ERR_INVALID_ARG), (dict(hq=0), E.DC_ERR_INVALID_ARG), (dict(hq=6), E.DC_ERR_SHAPE),
+    (dict(scale=0.0), E.DC_ERR_INVALID_ARG), (dict(scale=-1.0), E.DC_ERR_INVALID_ARG), (dict(scale=float("nan")), E.DC_ERR_INVALID_ARG),
+    (dict(scale=float("inf")), E.DC_ERR_INVALID_ARG), (dict(q=None), E.DC_ERR_INVALID_ARG), (dict(y=None), E.DC_ERR_INVALID_ARG),
+    (dict(ws=None), E.DC_ERR_INVALID_ARG), (dict(ws=0x180), E.DC_ERR_ALIGN), (dict(q=0x8000004), E.DC_ERR_ALIGN),
+    (dict(ys=1020), E.DC_ERR_SHAPE), (dict(ys=1026), E.DC_ERR_ALIGN), (dict(n=2, y=0x8000000), E.DC_ERR_INVALID_ARG),
+    (dict(n=2, nws=256), E.DC_ERR_BUFFER), (dict(n=1 << 30), E.DC_ERR_UNSUPPORTED),
+    (dict(b=batch(seqs=-1)), E.DC_ERR_INVALID_ARG), (dict(b=batch(groups=-1)), E.DC_ERR_INVALID_ARG),
+    (dict(b=batch(max_kv=-1)), E.DC_ERR_INVALID_ARG), (dict(b=batch(q_start=None)), E.DC_ERR_INVALID_ARG),
+    (dict(b=batch(kv_len=None)), E.DC_ERR_INVALID_ARG), (dict(b=batch(pages=None)), E.DC_ERR_INVALID_ARG),
+    (dict(b=batch(group_start=None)), E.DC_ERR_INVALID_ARG), (dict(b=batch(prefix_pages=None)), E.DC_ERR_INVALID_ARG),
+    (dict(b=batch(prefix_len=0x1402)), E.DC_ERR_ALIGN), (dict(b=batch(max_kv=129)), E.DC_ERR_SHAPE),
+    (dict(b=batch(max_prefix=65)), E.DC_ERR_SHAPE), (dict(b=batch(max_q=1 << 28)), E.DC_ERR_UNSUPPORTED),
+])
+def test_attention_refusals(L, kw, want):
+    assert attend(L, **kw) == want
+
+
+def test_attention_workspace(L):
+    c = cache()
+    size = lambda n=2, **kw: L.dc_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(batch(**kw)), 8, n)  # noqa: E731
+    assert size() > 256 and size() % 256 == 0
+    assert size(groups=0, max_kv=64) == 256            # one range of keys: no partial sums
+    assert size(n=2, max_kv=100) < size(n=4, max_kv=100)
+    need = size()
+    assert attend(L, n=2, nws=need - 1) == E.DC_ERR_BUFFER
+
+
+def w4(L, out=256, inn=384, base=0x1000000, x=0x2000000, y=0x3000000, t=0):
+    return L.dc_apply_w4(ctypes.byref(_lib.dc_w4_view(out, inn, base)), x, y, t, None)
+
+
+def test_w4_refusals(L):
+    assert trs.dc_w4_bytes(256, 384) == 256 * 384 // 2 + 4 * 256 * 3
+    assert [trs.dc_w4_bytes(*s) for s in ((0, 128), (128, 64), (130, 128), (-128, 128))] == [0] * 4
+    assert w4(L) == E.DC_OK
+    assert w4(L, t=-1) == E.DC_ERR_INVALID_ARG and w4(L, out=200) == E.DC_ERR_SHAPE
+    assert w4(L, base=None) == E.DC_ERR_INVALID_ARG and w4(L, x=None) == E.DC_ERR_INVALID_ARG
+    assert w4(L, x=0x2000004) == E.DC_ERR_ALIGN and w4(L, base=0x1000008) == E.DC_ERR_ALIGN
+    assert w4(L, t=4, y=0x2000010) == E.DC_ERR_INVALID_ARG
+    assert w4(L, out=1 << 16, inn=1 << 15) == E.DC_ERR_UNSUPPORTED
+    pack = lambda out=256, inn=384, w=0x1000000, d=0x2000000, n=1 << 30, f=0x100: L.dc_w4_pack_device(out, inn, w, d, n, f, None)  # noqa: E731
+    assert pack(out=100) == E.DC_ERR_SHAPE and pack(w=None) == E.DC_ERR_INVALID_ARG and pack(f=None) == E.DC_ERR_INVALID_ARG
+    assert pack(d=0x2000008) == E.DC_ERR_ALIGN and pack(n=trs.dc_w4_bytes(256, 384) - 1) == E.DC_ERR_BUFFER
+
+
+def test_binding_checks_types_and_shapes():
+    torch = pytest.importorskip("torch")
+    k = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+    c = trs.KvCache(k, k.clone())
+    assert (c.c.page_stride, c.c.head_stride, c.c.slot_stride) == (2048, 1024, 64)
+    one = torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16).transpose(1, 2)   # [pages][slots][heads][dim]
+    c = trs.KvCache(one, one.clone(memory_format=torch.preserve_format))
+    assert (c.c.page_stride, c.c.head_stride, c.c.slot_stride) == (2048, 64, 128)
+    with pytest.raises(ValueError):
+        trs.KvCache(k, k.float())
+    with pytest.raises(ValueError):
+        trs.KvCache(k.float(), k.float())
+    with pytest.raises(ValueError):
+        trs.KvCache(k, one)
+    with pytest.raises(ValueError):
+        trs.KvCache(k.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn), torch.ones(3), torch.ones(2))
+    with pytest.raises(ValueError):
+        trs.Rope(torch.ones(8))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError):
+        trs.AttnBatch(i32(2), i32(2), i32(2, 4), 1, 4)
+    with pytest.raises(ValueError):
+        trs.AttnBatch(i32(3), i32(2).long(), i32(2, 4), 1, 4)
+    with pytest.raises(ValueError):
+        trs.AttnBatch(i32(3), i32(2), i32(2, 4), 1, 4, group_start=i32(1), prefix_len=i32(1), prefix_pages=i32(1, 1))
+    with pytest.raises(ValueError):
+        trs.W4View(128, 128, torch.zeros(100, dtype=torch.uint8))
+    with pytest.raises(ValueError):   # rows that are too short for the heads
+        trs.dc_kv_append(c, None, torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16), None,
+                         torch.zeros(4, dtype=torch.int64), None, None)
