@@ -101,35 +101,35 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   AttnPlan p{};
   const int64_t ro = (int64_t)max_q * gq, rg = (int64_t)max_gq * gq;   // query rows of a sequence, of a group
   if (max_pre == 0 || max_gq == 0) G = 0;
-  // long queries: enough blocks of 256 rows for half the card
-  const int64_t rb = (ro + 255) / 256;
-  if (ro >= 64 && (int64_t)B * hkv * rb >= 128) {
+  // long queries: enough blocks of 128 rows to fill the card
+  const int64_t rb = (ro + 127) / 128;
+  if (ro > 32 && (int64_t)B * hkv * rb >= 256) {
     p.rows = true;
     p.rbo = (int32_t)rb;
-    p.co = p.cp = 32;
+    p.co = p.cp = 64;
     p.direct = true;
     return p;
   }
-  p.ro = ro <= 16 ? 1 : 2;
-  p.rp = p.ro == 2 ? 2 : (rg <= 16 ? 1 : (rg <= 32 ? 2 : 4));
-  p.rbo = (int32_t)((ro + 16 * p.ro - 1) / (16 * p.ro));
-  p.rbp = (int32_t)((rg + 16 * p.rp - 1) / (16 * p.rp));
+  p.to = ro > 16;
+  p.tp = p.to || rg > 16;
+  p.rbo = (int32_t)(p.to ? rb : (ro + 15) / 16);
+  p.rbp = (int32_t)(p.tp ? (rg + 127) / 128 : (rg + 15) / 16);
   // as many ranges as fill the card twice, each of 128 keys (a step a wave) or more
-  auto split = [](int64_t items, int64_t keys, int64_t want, int32_t* s, int32_t* c) {
+  auto split = [](int64_t items, int64_t keys, int32_t* s, int32_t* c) {
     if (items < 1) items = 1;
-    int64_t n = (want + items - 1) / items;
+    int64_t n = (512 + items - 1) / items;
     const int64_t most = (keys + 127) / 128;
     if (n > most) n = most;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
-    int64_t ch = ((keys + n - 1) / n + 31) / 32 * 32;
-    if (ch < 32) ch = 32;
+    int64_t ch = ((keys + n - 1) / n + 63) / 64 * 64;
+    if (ch < 64) ch = 64;
     *c = (int32_t)ch;
     *s = (int32_t)((keys + ch - 1) / ch);
   };
-  split((int64_t)B * hkv * p.rbo, max_kv, 512, &p.so, &p.co);
-  p.cp = 32;
-  if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, p.rp == 4 ? 256 : 512, &p.sp, &p.cp);
+  split((int64_t)B * hkv * p.rbo, max_kv, &p.so, &p.co);
+  p.cp = 64;
+  if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, &p.sp, &p.cp);
   if (p.sp == 0 && p.so <= 1) {
     p.so = 1;
     p.direct = true;

@@ -34,11 +34,11 @@ int launch_append(const AppendArgs& a);
 // How one attention call is split, from the host's bounds alone (the lengths
 // stay on the device).
 struct AttnPlan {
-  bool rows;          // long queries: a block walks all keys of its rows; else the keys are split
-  int32_t ro, rp;     // split form: 16-row tiles a wave holds, own keys / prefix
+  bool rows;          // long queries: a block walks all keys of its 128 rows; else the keys are split
+  bool to, tp;        // split form: own keys / prefixes by Tiles (to: both), else by Keys
   int32_t rbo, rbp;   // row blocks of a sequence / of a group
   int32_t so, sp;     // key splits of a sequence's own keys / of a prefix
-  int32_t co, cp;     // keys of a split (multiples of 32)
+  int32_t co, cp;     // keys of a split (multiples of 64)
   bool direct;        // one split in all: the outputs are written at once
   size_t o_off, ws;   // split form: partial sums at o_off of the workspace, its size
 };
