@@ -591,14 +591,24 @@ def _typed(t, what: str, names, contiguous: bool = True):
 
 
 _BF16 = ("bfloat16", "int16", "uint16")   # bf16 tensors, or their bits
+_torch = None
+_bf16_types = ()
+
+
+def _load_torch():
+    global _torch, _bf16_types
+    import torch
+    _bf16_types = tuple(getattr(torch, n) for n in _BF16)
+    _torch = torch
+    return torch
 
 
 def _current(device: int, stream) -> int:
     """The stream of a call on tensors of `device`, which must be current."""
-    import torch
-    if torch.cuda.current_device() != device:
-        raise ValueError("the tensors are on device %d, the current one is %d" % (device, torch.cuda.current_device()))
-    return int(stream) if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    c = (_torch or _load_torch())._C
+    if c._cuda_getDevice() != device:
+        raise ValueError("the tensors are on device %d, the current one is %d" % (device, c._cuda_getDevice()))
+    return int(stream) if stream is not None else c._cuda_getCurrentRawStream(device)
 
 
 def _same_device(device: int, **ts) -> None:
@@ -649,13 +659,23 @@ class Rope:
         self.ref = ctypes.byref(self.c)
 
 
-def _rows(t, what: str, n: int, cols: int) -> int:
+def _rows(t, what: str, n: int, cols: int, device: int) -> int:
     """The row stride of bf16 rows [n][cols] (heads side by side)."""
-    if t.dim() != 2 or t.shape[0] != n or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be [%d][%d] with contiguous rows" % (what, n, cols))
-    if str(t.dtype)[6:] not in _BF16:
-        raise ValueError("%s must be bf16" % what)
-    return t.stride(0) if n > 1 else cols
+    if _torch is None:
+        _load_torch()
+    if t.shape != (n, cols) or t.dtype not in _bf16_types or t.get_device() != device:
+        raise ValueError("%s must be bf16 [%d][%d] on device %d" % (what, n, cols, device))
+    stride, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("the rows of %s must be contiguous" % what)
+    return stride if n > 1 else cols
+
+
+def _vector(t, what: str, n: int, dtype, device: int) -> int:
+    """The address of a contiguous vector of n elements."""
+    if t.shape != (n,) or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s [%d] on device %d" % (what, dtype, n, device))
+    return t.data_ptr()
 
 
 def dc_kv_append(cache: KvCache, q, k, v, pos, slots, rope: Rope, q_out, stream=None) -> None:
@@ -663,24 +683,25 @@ def dc_kv_append(cache: KvCache, q, k, v, pos, slots, rope: Rope, q_out, stream=
     v into the cache at slots.  q, q_out [N][q_heads*dim], k, v
     [N][heads*dim] bf16 rows of any stride; q = q_out = None: no queries.  pos
     int32 [N], slots int64 [N]; rope None: no rotation (pos may be None)."""
-    n = k.shape[0]
-    kc = cache.heads * cache.dim
-    ks, vs = _rows(k, "k", n, kc), _rows(v, "v", n, kc)
-    _same_device(cache.device, q=q, k=k, v=v, pos=pos, slots=slots, q_out=q_out)
-    if rope is not None and (rope.device != cache.device or pos is None):
-        raise ValueError("the rotation needs pos and its frequencies on the cache's device")
-    if _typed(slots, "slots", ("int64",)).numel() != n or (
-            pos is not None and _typed(pos, "pos", ("int32",)).numel() != n):
-        raise ValueError("slots and pos must have one entry a token")
+    n, dev, kc = k.shape[0], cache.device, cache.heads * cache.dim
+    ks, vs = _rows(k, "k", n, kc, dev), _rows(v, "v", n, kc, dev)
+    ps = _vector(slots, "slots", n, _torch.int64, dev)
+    pp = pr = None
+    if rope is not None:
+        if rope.device != dev or pos is None:
+            raise ValueError("the rotation needs pos, and its frequencies on the cache's device")
+        pp, pr = _vector(pos, "pos", n, _torch.int32, dev), rope.ref
     hq = qs = qos = 0
+    pq = po = None
     if q is not None:
-        hq = q.shape[1] // cache.dim
-        qs, qos = _rows(q, "q", n, hq * cache.dim), _rows(q_out, "q_out", n, hq * cache.dim)
-    _check(lib().dc_kv_append(cache.ref, rope.ref if rope is not None else None,
-                              q.data_ptr() if hq else None, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                              pos.data_ptr() if pos is not None else None, slots.data_ptr(),
-                              q_out.data_ptr() if hq else None, qos, hq, n, _current(cache.device, stream)),
-           "dc_kv_append")
+        cols = q.shape[1]
+        hq = cols // cache.dim
+        if cols != hq * cache.dim:
+            raise ValueError("q must have whole heads of %d" % cache.dim)
+        qs, qos = _rows(q, "q", n, cols, dev), _rows(q_out, "q_out", n, cols, dev)
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    _check(lib().dc_kv_append(cache.ref, pr, pq, qs, k.data_ptr(), ks, v.data_ptr(), vs, pp, ps, po, qos, hq, n,
+                              _current(dev, stream)), "dc_kv_append")
 
 
 class AttnBatch:
@@ -725,13 +746,15 @@ def dc_attention(cache: KvCache, q, batch: AttnBatch, scale: float, y, ws, strea
     """y = softmax(scale q k) v over the cache: q and y [N][q_heads*dim] bf16
     rows of any stride."""
     n, cols = q.shape
+    dev = cache.device
     hq = cols // cache.dim
-    qs, ys = _rows(q, "q", n, hq * cache.dim), _rows(y, "y", n, hq * cache.dim)
-    if batch.device != cache.device:
-        raise ValueError("the batch and the cache are on different devices")
-    _same_device(cache.device, q=q, y=y, ws=ws)
+    if cols != hq * cache.dim:
+        raise ValueError("q must have whole heads of %d" % cache.dim)
+    qs, ys = _rows(q, "q", n, cols, dev), _rows(y, "y", n, cols, dev)
+    if batch.device != dev or ws.get_device() != dev:
+        raise ValueError("the batch, the workspace and the cache must be on one device")
     _check(lib().dc_attention(cache.ref, batch.ref, q.data_ptr(), qs, hq, scale, y.data_ptr(), ys, n, _dptr(ws, "ws"),
-                              ws.numel() * ws.element_size(), _current(cache.device, stream)), "dc_attention")
+                              ws.numel() * ws.element_size(), _current(dev, stream)), "dc_attention")
 
 
 # ---------------------------------------------------------- 4-bit backbone
@@ -765,10 +788,7 @@ def dc_w4_pack_device(W, dst, flag, stream=None) -> None:
 
 def dc_apply_w4(view: W4View, x, y, stream=None) -> None:
     """y [T][out] = W x, x [T][in], both bf16 and contiguous."""
-    t = x.shape[0]
-    if x.dim() != 2 or x.shape[1] != view.inn or y.shape != (t, view.out):
-        raise ValueError("x must be [T][%d] and y [T][%d]" % (view.inn, view.out))
-    _typed(x, "x", _BF16)
-    _typed(y, "y", _BF16)
-    _same_device(view.device, x=x, y=y)
-    _check(lib().dc_apply_w4(view.ref, x.data_ptr(), y.data_ptr(), t, _current(view.device, stream)), "dc_apply_w4")
+    t, dev = x.shape[0], view.device
+    if _rows(x, "x", t, view.inn, dev) != view.inn or _rows(y, "y", t, view.out, dev) != view.out:
+        raise ValueError("x and y must be contiguous")
+    _check(lib().dc_apply_w4(view.ref, x.data_ptr(), y.data_ptr(), t, _current(dev, stream)), "dc_apply_w4")

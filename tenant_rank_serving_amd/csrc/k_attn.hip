@@ -146,49 +146,87 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int n
   if constexpr (!TO || !TP) keys_block<D, F8>(a, it, row0, h, c0, c1, slot, sh.keys);
 }
 
-// Joins the splits of a row: one wave a row, D/64 elements a lane.
+// Joins the splits of a row: one wave a row.  Everything that does not depend
+// on the token's sequence is loaded at once: the sequences' starts and
+// lengths (64 at a time, one a lane), the splits' maxima and weights (one a
+// lane) and the first of their sums.  A half wave takes every other split, 16
+// bytes a lane (D = 64: a quarter, every fourth).
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
+  constexpr int L = D / 4, P = 64 / L;   // lanes of a split's sums, splits at a time
+  constexpr int kAhead = 4;
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= (int64_t)a.n * a.hq) return;
   const int tok = (int)(row / a.hq), h = (int)(row - (int64_t)tok * a.hq);
+  const int sp = a.plan.sp, slots = sp + a.plan.so;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.pml) + row * slots;
+  const float* po = a.po + row * slots * D + (lane % L) * 4;
+  // slots lane and lane + 64 (a prefix and the own keys have at most 64 each)
+  const f32x2 mla = ml[min(lane, slots - 1)], mlb = ml[min(lane + 64, slots - 1)];
+  f32x4 first[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    first[i] = *reinterpret_cast<const f32x4*>(po + (int64_t)min(i * P + lane / L, slots - 1) * D);
   // the token's sequence: the last one that starts at or before it
-  int b = -1;
+  int b = -1, len = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int i = b0 + lane;
-    const bool in = i < a.B && a.q_start[i] <= tok && tok < a.q_start[i + 1];
+    const int i = min(b0 + lane, a.B - 1);
+    const int s = a.q_start[i], e = a.q_start[i + 1], n = a.kv_len[i];
+    const bool in = b0 + lane < a.B && s <= tok && tok < e && tok - clampi(s, 0, a.n) < a.max_q;
     const uint64_t hit = __builtin_amdgcn_ballot_w64(in);
-    if (hit) b = b0 + 63 - __builtin_clzll(hit);
+    if (hit) {
+      const int at = 63 - __builtin_clzll(hit);
+      b = b0 + at;
+      len = __builtin_amdgcn_readlane(n, at);
+    }
+  }
+  int plen = 0;
+  for (int g0 = 0; g0 < a.G; g0 += 64) {
+    const int g = min(g0 + lane, a.G - 1);
+    const int n = a.p_len[g];
+    const bool in = g0 + lane < a.G && a.g_start[g] <= b && b < a.g_start[g + 1];
+    const uint64_t hit = __builtin_amdgcn_ballot_w64(in);
+    if (hit) plen = __builtin_amdgcn_readlane(n, 63 - __builtin_clzll(hit));
   }
   if (b < 0) return;   // behind the last sequence: left as it is
-  const Item it = own_item(a, b);
-  if (tok - it.t0 >= it.nt) return;
-  const int no = (it.len + a.plan.co - 1) / a.plan.co;
-  int np = 0;
-  const int gr = group_of(a, b);
-  if (gr >= 0) np = (clampi(a.p_len[gr], 0, a.max_pre) + a.plan.cp - 1) / a.plan.cp;
-  const int slots = a.plan.sp + a.plan.so;
-  const float* ml = a.pml + 2 * row * slots;
-  const float* o = a.po + row * slots * D + lane * (D / 64);
-  float m = kLow, l = 0.f, x[D / 64];
+  const int no = (clampi(len, 0, a.max_kv) + a.plan.co - 1) / a.plan.co;
+  const int np = (clampi(plen, 0, a.max_pre) + a.plan.cp - 1) / a.plan.cp;
+  // splits that hold keys were written by their blocks
+  auto held = [&](int s) __attribute__((always_inline)) { return s < np || (s >= sp && s - sp < no); };
+  float ma = held(lane) ? mla[0] : kLow, mb = held(lane + 64) ? mlb[0] : kLow;
+  float m = fmaxf(ma, mb);
 #pragma unroll
-  for (int j = 0; j < D / 64; ++j) x[j] = 0.f;
-  for (int s = 0; s < slots; ++s)
-    if (s < np || (s >= a.plan.sp && s - a.plan.sp < no)) m = fmaxf(m, ml[2 * s]);
-  for (int s = 0; s < slots; ++s) {
-    if (!(s < np || (s >= a.plan.sp && s - a.plan.sp < no))) continue;
-    const float f = __builtin_amdgcn_exp2f(ml[2 * s] - m);
-    l += ml[2 * s + 1] * f;
+  for (int i = 1; i < 64; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
+  const float wa = held(lane) ? __builtin_amdgcn_exp2f(ma - m) : 0.f;
+  const float wb = held(lane + 64) ? __builtin_amdgcn_exp2f(mb - m) : 0.f;
+  float l = (held(lane) ? mla[1] * wa : 0.f) + (held(lane + 64) ? mlb[1] * wb : 0.f);
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) x[j] += o[(int64_t)s * D + j] * f;
+  for (int i = 1; i < 64; i <<= 1) l += __shfl_xor(l, i);
+  f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < slots; s0 += P * kAhead) {
+    f32x4 o[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i * P + lane / L;
+      o[i] = s0 == 0 ? first[i] : *reinterpret_cast<const f32x4*>(po + (int64_t)min(s, slots - 1) * D);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i * P + lane / L;
+      const float w = s < 64 ? __shfl(wa, s & 63) : __shfl(wb, s & 63);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] += held(s) ? o[i][j] * w : 0.f;
+    }
   }
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* y = a.y + (int64_t)tok * a.ys + (int64_t)h * D + lane * (D / 64);
-  if constexpr (D == 128)
-    *reinterpret_cast<uint32_t*>(y) = pack2(x[0] * f, x[1] * f);
-  else
-    *y = (uint16_t)pack2(x[0] * f, 0.f);
+#pragma unroll
+  for (int i = L; i < 64; i <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] += __shfl_xor(x[j], i);
+  if (lane < L) {
+    const float xs[4] = {x[0], x[1], x[2], x[3]};
+    store_y<4>(a.y + (int64_t)tok * a.ys + (int64_t)h * D + lane * 4, xs, l == 0.f ? 0.f : 1.f / l);
+  }
 }
 
 // Long queries.  Blocks of one (sequence, kv head) follow each other on one

@@ -34,13 +34,14 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
 }
 
 // Block: RT 16-row tiles of the matrix x TT 16-token tiles, all inputs; NW
-// waves take the 128-groups in turn (wave w: groups w, w + NW, ..) and add
-// their sums through LDS, so a call is one launch without a workspace.
+// waves take the 128-groups in turn (wave w: groups w, w + NW, ..), U of its
+// groups at a time with all their loads issued first, and add their sums
+// through LDS, so a call is one launch without a workspace.
 // Operands: lane l holds row (token) l%16 and columns 32(l/16) + 8j .. +8 of
 // the group for op j; result: token l%16, rows 4(l/16) .. +4.
-template <int RT, int TT, int NW>
-__global__ void __launch_bounds__(64 * NW) k_w4(const uint8_t* __restrict__ wq, const uint16_t* __restrict__ x,
-                                                uint16_t* __restrict__ y, int out, int in, int T) {
+template <int RT, int TT, int NW, int U>
+__global__ void __launch_bounds__(64 * NW, NW / 4) k_w4(const uint8_t* __restrict__ wq, const uint16_t* __restrict__ x,
+                                                        uint16_t* __restrict__ y, int out, int in, int T) {
   __shared__ float red[NW][RT * 16][TT * 16 + 1];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int r0 = blockIdx.x * RT * 16, t0 = blockIdx.y * TT * 16;
@@ -59,32 +60,53 @@ __global__ void __launch_bounds__(64 * NW) k_w4(const uint8_t* __restrict__ wq, 
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int t = 0; t < TT; ++t) tot[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int g = wave; g < gi; g += NW) {
-    uint4 w[RT], s4[RT];
+  for (int g0 = wave; g0 < gi; g0 += NW * U) {
+    uint4 w[U][RT], s4[U][RT];
+    bf16x8 b[U][TT][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int row = r0 + 16 * min(r, rt - 1);
-      w[r] = *reinterpret_cast<const uint4*>(wq + ((size_t)(row / 16) * gi + g) * 1024 + lane * 16);
-      s4[r] = *reinterpret_cast<const uint4*>(sz + (size_t)g * out + row + 4 * (lane >> 4));
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      bf16x8 b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const bf16x8*>(xp[t] + (size_t)g * kGroup + 8 * j);
-      f32x4 xs = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) xs = mfma(ones, b[j], xs);
+    for (int u = 0; u < U; ++u) {
+      const int g = min(g0 + u * NW, gi - 1);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const uint32_t ww[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-        f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int row = r0 + 16 * min(r, rt - 1);
+        w[u][r] = *reinterpret_cast<const uint4*>(wq + ((size_t)(row / 16) * gi + g) * 1024 + lane * 16);
+        s4[u][r] = *reinterpret_cast<const uint4*>(sz + (size_t)g * out + row + 4 * (lane >> 4));
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc = mfma(codes8(ww[j]), b[j], acc);
-        const uint32_t zz[4] = {s4[r].x, s4[r].y, s4[r].z, s4[r].w};
+      for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          tot[r][t][i] += h2f(zz[i] & 0xFFFFu) * (acc[i] - (128.f + h2f(zz[i] >> 16)) * xs[i]);
+        for (int j = 0; j < 4; ++j) b[u][t][j] = *reinterpret_cast<const bf16x8*>(xp[t] + (size_t)g * kGroup + 8 * j);
+    }
+    __builtin_amdgcn_sched_barrier(0);   // the loads stay ahead of the products
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (U > 1 && g0 + u * NW >= gi) break;
+      f32x4 xs[TT];   // the group's sums of x, the same for every row
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        xs[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xs[t] = mfma(ones, b[u][t][j], xs[t]);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t ww[4] = {w[u][r].x, w[u][r].y, w[u][r].z, w[u][r].w};
+        const uint32_t zz[4] = {s4[u][r].x, s4[u][r].y, s4[u][r].z, s4[u][r].w};
+        f32x4 acc[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 c = codes8(ww[j]);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) acc[t] = mfma(c, b[u][t][j], acc[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s = h2f(zz[i] & 0xFFFFu), z = 128.f + h2f(zz[i] >> 16);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) tot[r][t][i] += s * (acc[t][i] - z * xs[t][i]);
+        }
       }
     }
   }
@@ -153,19 +175,19 @@ __global__ void __launch_bounds__(256) k_w4_pack(const uint16_t* __restrict__ W,
 
 __global__ void k_w4_flag(uint32_t* flag) { *flag = 0; }
 
-template <int RT, int TT, int NW>
+template <int RT, int TT, int NW, int U>
 void go(const W4Args& a) {
   const dim3 g((unsigned)((a.out + RT * 16 - 1) / (RT * 16)), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
-  hipLaunchKernelGGL((k_w4<RT, TT, NW>), g, dim3(64 * NW), 0, reinterpret_cast<hipStream_t>(a.stream), a.w, a.x, a.y,
+  hipLaunchKernelGGL((k_w4<RT, TT, NW, U>), g, dim3(64 * NW), 0, reinterpret_cast<hipStream_t>(a.stream), a.w, a.x, a.y,
                      a.out, a.in, a.T);
 }
 
 }  // namespace
 
 int launch_w4(const W4Args& a) {
-  if (a.T <= 16) go<1, 1, 8>(a);
-  else if (a.T <= 32) go<1, 2, 8>(a);
-  else go<2, 4, 8>(a);
+  if (a.T <= 16) go<1, 1, 8, 4>(a);
+  else if (a.T <= 32) go<2, 2, 8, 2>(a);
+  else go<4, 4, 8, 1>(a);
   return (int)hipGetLastError();
 }
 
