@@ -11,8 +11,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kLow = -3.402823466e38f;   // the maximum of a row that has seen no key
 // The running maximum of a row moves only when a score passes it by this
 // (in powers of 2): most steps then leave the sums as they are, and a weight
-// reaches 2^6 instead of 1, which floats do not mind.
-constexpr float kSlack = 6.f;
+// reaches 2^12 instead of 1, which floats do not mind.
+constexpr float kSlack = 12.f;
 constexpr int kWaves = 4;
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {   // round to nearest even

@@ -197,7 +197,7 @@ struct Keys {
 template <int D>
 struct KeysLds {
   float ml[kWaves][16][2];
-  float o[kWaves][16][D + 4];
+  alignas(16) float o[kWaves][16][D + 4];
 };
 template <int D, bool F8, class Put>
 __device__ __forceinline__ void join(const Keys<D, F8>& R, KeysLds<D>& sh, Put put) {
