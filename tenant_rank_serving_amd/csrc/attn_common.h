@@ -64,30 +64,17 @@ struct Stream {
   int64_t page_stride;
   int32_t slot_stride;      // a page's slots lie within 2^31 bytes
   const int32_t* table;
-  int32_t npages;           // entries of the table that hold keys
+  int32_t width;            // entries of the table (those that hold no keys are read, not used)
   int32_t num_pages;        // pages of the cache
   int32_t shift;            // log2 of a page's slots
 };
-
-__device__ __forceinline__ Stream stream_of(const AttnArgs& a, int h, const int32_t* table, int len) {
-  Stream st;
-  st.k = a.kv.k + h * a.kv.head_stride;
-  st.v = a.kv.v + h * a.kv.head_stride;
-  st.page_stride = a.kv.page_stride;
-  st.slot_stride = (int)a.kv.slot_stride;
-  st.table = table;
-  st.shift = a.kv.shift;
-  st.npages = ((len - 1) >> st.shift) + 1;
-  st.num_pages = a.kv.num_pages;
-  return st;
-}
 
 // A stream's page numbers, 64 of them in a register, one a lane.
 struct Pages {
   int base, pg;
   __device__ __forceinline__ void fill(const Stream& st, int p) {
     base = p;
-    pg = st.table[min(p + (int)(threadIdx.x & 63), st.npages - 1)];
+    pg = st.table[min(p + (int)(threadIdx.x & 63), st.width - 1)];
     pg = (unsigned)pg < (unsigned)st.num_pages ? pg : 0;   // never outside the cache
   }
   // Byte offset of key `at` (the first of 16 that share a page); ascending.
@@ -105,7 +92,7 @@ struct Pages {
 // element by element.  (A weight is positive, so the value stands for weight
 // times value.)
 __device__ __forceinline__ const uint8_t* value_row(const Stream& st, int key) {
-  int pg = st.table[min(key >> st.shift, st.npages - 1)];
+  int pg = st.table[min(key >> st.shift, st.width - 1)];
   pg = (unsigned)pg < (unsigned)st.num_pages ? pg : 0;
   return st.v + pg * st.page_stride + (int64_t)(key & ((1 << st.shift) - 1)) * st.slot_stride;
 }
@@ -124,9 +111,23 @@ struct Item {
   int32_t first;          // own keys: token j sees first + j + 1 of them
   bool causal;
   const int32_t* table;
-  // keys that row r sees
+  int32_t width;
+  // keys that token tok sees
   __device__ __forceinline__ int sees(int tok) const { return causal ? clampi(first + tok + 1, 0, len) : len; }
 };
+
+__device__ __forceinline__ Stream stream_of(const AttnArgs& a, int h, const Item& it) {
+  Stream st;
+  st.k = a.kv.k + h * a.kv.head_stride;
+  st.v = a.kv.v + h * a.kv.head_stride;
+  st.page_stride = a.kv.page_stride;
+  st.slot_stride = (int)a.kv.slot_stride;
+  st.table = it.table;
+  st.width = it.width;
+  st.shift = a.kv.shift;
+  st.num_pages = a.kv.num_pages;
+  return st;
+}
 
 // Sequence b with its own keys; what the bounds do not cover is cut.
 __device__ __forceinline__ Item own_item(const AttnArgs& a, int b) {
@@ -139,6 +140,7 @@ __device__ __forceinline__ Item own_item(const AttnArgs& a, int b) {
   it.first = it.len - it.nt;
   it.causal = true;
   it.table = a.pages + (int64_t)b * a.pw;
+  it.width = a.pw;
   return it;
 }
 // The tokens of group g's sequences with its prefix.
@@ -153,6 +155,7 @@ __device__ __forceinline__ Item prefix_item(const AttnArgs& a, int g) {
   it.first = 0;
   it.causal = false;
   it.table = a.p_pages + (int64_t)g * a.ppw;
+  it.width = a.ppw;
   return it;
 }
 

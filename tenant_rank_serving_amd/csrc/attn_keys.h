@@ -39,7 +39,7 @@ struct Keys {
   __device__ __forceinline__ void start(const AttnArgs& a, const Item& it, int row0, int h, uint32_t flip) {
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const int row = min(row0 + (lane & 15), it.rows - 1);   // past the last row: the last one again
-    const int tok = row / a.gq, hh = row - tok * a.gq;
+    const int tok = a.gq_d.of(row), hh = row - tok * a.gq;
     const uint16_t* p = a.q + (int64_t)(it.t0 + tok) * a.qs + (int64_t)(h * a.gq + hh) * D;
 #pragma unroll
     for (int i = 0; i < C; ++i) {

@@ -9,13 +9,15 @@
 //   P^T operand B: row l%32, 8 keys of half l/32: results 8a .. 8a+7 as they
 //       are, so product a of a 32-key half takes keys 16a + 4(l/32) + {0..3}
 //       and those + 8.
-//   LDS holds K as [64 keys][D] and V^T as [D][64 keys in that order], both
-//       bf16 (e4m3 codes are converted on the way in, once a block), in lines
-//       of 256 bytes, the width of the banks; the 16 pieces of a line are
-//       permuted by an XOR such that 16 neighbouring lanes reach 16 different
-//       ones, in the reads and in the writes (key_at, value_at).
-// V is transposed on the way in: a thread loads 8 keys x D/32 elements and
-// writes D/32 pieces.
+//   V^T operand A: element 32 d + l%32, the same 8 keys: two transposing reads
+//       of LDS (ds_read_b64_tr_b16: of 16 lanes, lane 4r + c supplies elements
+//       4c .. 4c+3 of row r, lane j receives element j of the 4 rows).
+//   LDS holds K and V as the cache does, [64 keys][D] in bf16, the 16-byte
+//       pieces of a key permuted by an XOR with its number such that the lanes
+//       that are served together reach different banks (key_swizzle,
+//       value_swizzle).  bf16 keys go straight to LDS (global_load_lds, no
+//       registers; the lanes choose the permuted pieces); e4m3 codes pass
+//       through registers and are converted, once a block.
 #pragma once
 
 __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
@@ -26,24 +28,18 @@ constexpr int kTile = 64;        // keys of a tile
 constexpr int kTileRows = 32;    // rows of a wave
 constexpr int kBlockRows = kWaves * kTileRows;
 
-// A line holds one key of D = 128, or keys i and i + 16 of a half of D = 64.
-template <int D> __device__ __forceinline__ int key_at(int key, int c) {
-  if constexpr (D == 128) return key * 256 + ((c ^ (key & 15)) * 16);
-  const int line = key & 15, f = ((line & 1) << 3) | (line >> 1);
-  return (key >> 5) * 4096 + line * 256 + (((((key >> 4) & 1) * 8 + c) ^ f) * 16);
-}
-// Element d's values, 8 keys (piece kg): regions of 32 elements, a line holds
-// elements i and i + 16 of it; the regions are 64 bytes apart in the banks.
-constexpr int kRegion = 4096 + 64;
-template <int D> __device__ __forceinline__ int value_at(int d, int kg) {
-  const int line = d & 15, f = D == 128 ? (line >> 2) | ((line & 3) << 2) : ((line & 1) << 3) | (line >> 1);
-  return (d >> 5) * kRegion + line * 256 + (((((d >> 4) & 1) * 8 + kg) ^ f) * 16);
+// What a key's number is XOR-ed into the numbers of its pieces.  A read of K
+// serves 16 keys' pieces of one number at a time, a transposing read of V 64
+// bytes of 4 keys; the banks are 256 bytes wide (a key, or two of D = 64).
+template <int D> __device__ __forceinline__ int key_swizzle(int key) { return D == 128 ? key & 15 : (key >> 1) & 7; }
+template <int D> __device__ __forceinline__ int value_swizzle(int key) {
+  return D == 128 ? (key & 3) << 2 : ((key >> 1) & 1) << 2;
 }
 
 template <int D>
 struct TilesLds {
   alignas(256) uint8_t k[2][kTile * D * 2];
-  alignas(256) uint8_t v[2][D / 32 * kRegion];
+  alignas(256) uint8_t v[2][kTile * D * 2];
   uint32_t odd[2][kWaves];       // of a tile with masks: some of the values that a wave carried are not finite
 };
 
@@ -68,7 +64,7 @@ struct Tiles {
   __device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int row0, int h, uint32_t flip) {
     const int lane = threadIdx.x & 63;
     const int row = min(row0 + (lane & 31), it.rows - 1);   // past the last row: the last one again
-    const int tok = row / a.gq, hh = row - tok * a.gq;
+    const int tok = a.gq_d.of(row), hh = row - tok * a.gq;
     const uint16_t* p = a.q + (int64_t)(it.t0 + tok) * a.qs + (int64_t)(h * a.gq + hh) * D + 8 * (lane >> 5);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
@@ -85,124 +81,163 @@ struct Tiles {
   // exponentials of half h and multiplies its values, in one stretch of code
   // without branches, so that the matrix core and the vector unit work at the
   // same time within a wave.  What a maximum moves is decided between steps.
-  // K of the next tile is stored to LDS in a tile's first step and needed in
-  // its second, V is stored in the second and needed in the next tile's first:
-  // with two buffers, one barrier a step.
+  // K of the next tile is needed in a tile's second step and V in the next
+  // tile's first; each is on its way for two steps.  With two buffers, one
+  // barrier a step.
   __device__ __forceinline__ void walk(const Stream& st, int k0, int k1, int lo, int up, int blo, int bup, float c,
                                        bool live, TilesLds<D>& sh) {
     k1 = min(k1, bup);
     if (k0 >= k1) return;
-    Stage g(st);
+    Stage g(st, sh);
     const int lane = threadIdx.x & 63, half = lane >> 5, i32 = lane & 31;
-    int ko[KS], vo[4];
+    int ko[KS], vo[DT];
 #pragma unroll
-    for (int i = 0; i < KS; ++i) ko[i] = key_at<D>(i32, 2 * i + half);
+    for (int i = 0; i < KS; ++i) ko[i] = i32 * (D * 2) + (((2 * i + half) ^ key_swizzle<D>(i32)) * 16);
+    const int r = (lane & 15) >> 2;   // a transposing read: the lane's key of 4, its 8 bytes of 32
 #pragma unroll
-    for (int a = 0; a < 4; ++a) vo[a] = value_at<D>(i32, 2 * a + half);
+    for (int d = 0; d < DT; ++d)
+      vo[d] = (4 * half + r) * (D * 2) +
+              (((4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<D>(r)) * 16) + (lane & 1) * 8;
     if (!live) up = k0;   // no key is of interest
-    g.load_k(st, k0, k1);
-    g.load_v(st);
+    g.load_k(st, k0, k1, g.k_at(sh, 0));
+    g.load_v(st, g.v_at(sh, 0));
     g.store_k(sh.k[0]);
-    g.store_v(sh.v[0], sh.odd[0], k0, blo, bup);
-    if (k0 + kTile < k1) g.load_k(st, k0 + kTile, k1);
-    __syncthreads();
+    g.store_v(sh.v[0]);
+    wait_loads<0>();
+    g.mend_v(sh.v[0], sh.odd[0], k0, blo, bup);
+    if (k0 + kTile < k1) g.load_k(st, k0 + kTile, k1, g.k_at(sh, 1));
+    wait_lds_barrier();
     f32x16 s;
     if (k0 < up) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
       for (int i = 0; i < KS; ++i) s = mfma32(*reinterpret_cast<const uint4*>(sh.k[0] + ko[i]), q[i], s);
-      prepare(s, k0, lo, c);
+      prepare(s, largest(s), k0, lo, c);
     }
     for (int k = k0; k < k1; k += 2 * kTile) {
       tile<0>(g, st, s, k, k1, lo, up, blo, bup, c, ko, vo, sh);
       if (k + kTile < k1) tile<1>(g, st, s, k + kTile, k1, lo, up, blo, bup, c, ko, vo, sh);
     }
-    __syncthreads();   // the buffers are free
+    wait_lds_barrier();   // the buffers are free
   }
 
  private:
   static constexpr int KB = F8 ? 1 : 2;              // bytes of an element of the cache
   static constexpr int KL = 16 * D * KB / 1024;      // 16-byte pieces of a wave's 16 keys, a lane
   static constexpr int KP = D * KB / 16;             // pieces of a key
-  static constexpr int DW = D / 32;                  // elements of a lane's piece of a value
-  static constexpr int VW = DW * KB / 4;             // its words (0: half a word)
+  static constexpr int KI = 64 / KP;                 // keys of a wave's load
+
+  // At most N loads of the wave still on their way.
+  template <int N> static __device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  }
+  // The wave's own LDS accesses are done, and so are every other wave's.
+  static __device__ __forceinline__ void wait_lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
 
   // A wave's part of a tile on its way from the cache to LDS: wave w carries
   // keys 16w .. 16w+15 (one page).
   struct Stage {
-    Words<4> kr[KL];
-    Words<VW> vr[8];
+    Words<4> kr[F8 ? KL : 1], vr[F8 ? KL : 1];   // e4m3: codes to be converted
     Pages pages;
-    const uint8_t* vp;
-    int koff, voff, wave;
-    __device__ __forceinline__ Stage(const Stream& st) {
+    int64_t off;
+    int wave, ko[F8 ? 1 : KL], vo;   // the lane's offsets in 16 keys' rows
+    __device__ __forceinline__ Stage(const Stream& st, const TilesLds<D>& sh) {
       const int lane = threadIdx.x & 63;
       wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-      koff = (lane / KP) * st.slot_stride + (lane % KP) * 16;
-      voff = 4 * (lane >> 5) * st.slot_stride + (lane & 31) * (DW * KB);
       pages.base = -64;
-    }
-    // the keys of the tile at k, and where its values are
-    __device__ __forceinline__ void load_k(const Stream& st, int k, int k1) {
-      const int64_t off = pages.offset(st, min(k + 16 * wave, (k1 - 1) & ~15));
-      vp = st.v + off;
+      base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)&sh.k[0][0] + wave * (16 * D * 2);
+      const int key = lane / KP, pos = lane % KP;   // LDS takes 16 bytes a lane, in the order of the lanes
+      if constexpr (F8) {
+        ko[0] = vo = key * st.slot_stride + pos * 16;
+      } else {
 #pragma unroll
-      for (int i = 0; i < KL; ++i) kr[i] = load_words<4>(st.k + off + (int64_t)(64 / KP * i) * st.slot_stride + koff);
+        for (int i = 0; i < KL; ++i) ko[i] = key * st.slot_stride + (pos ^ key_swizzle<D>(key + KI * i)) * 16;
+        vo = key * st.slot_stride + (pos ^ value_swizzle<D>(key)) * 16;
+      }
     }
-    // the values of the tile whose keys were loaded last
-    __device__ __forceinline__ void load_v(const Stream& st) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) vr[e] = load_words<VW>(vp + (int64_t)((e & 3) + 8 * (e >> 2)) * st.slot_stride + voff);
+    // LDS addresses of the wave's part of buffer b
+    uint32_t base;
+    __device__ __forceinline__ uint32_t k_at(const TilesLds<D>& sh, int b) const { return base + b * (kTile * D * 2); }
+    __device__ __forceinline__ uint32_t v_at(const TilesLds<D>& sh, int b) const {
+      return base + (uint32_t)sizeof(sh.k) + b * (kTile * D * 2);
     }
-    __device__ __forceinline__ void store_k(uint8_t* lds) {
-      const int lane = threadIdx.x & 63;
+    // 16 bytes a lane from base + voff to lds + 16 lane
+    static __device__ __forceinline__ void to_lds(const uint8_t* base, int voff, uint32_t at) {
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(voff), "s"(base) : "memory");
+    }
+    // the keys of the tile at k, and where its values are; at: where in LDS
+    // the wave's part begins
+    __device__ __forceinline__ void load_k(const Stream& st, int k, int k1, uint32_t at) {
+      off = pages.offset(st, min(k + 16 * wave, (k1 - 1) & ~15));
 #pragma unroll
       for (int i = 0; i < KL; ++i) {
-        const int key = 16 * wave + lane / KP + 64 / KP * i, cc = lane % KP;
-        if constexpr (F8) {
+        const uint8_t* p = st.k + off + (int64_t)(KI * i) * st.slot_stride;
+        if constexpr (F8) kr[i] = load_words<4>(p + ko[0]);
+        else to_lds(p, ko[i], at + i * 1024);
+      }
+    }
+    // the values of the tile whose keys were loaded last
+    __device__ __forceinline__ void load_v(const Stream& st, uint32_t at) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<uint4*>(lds + key_at<D>(key, 2 * cc + u)) =
-                uint4{cvt2(kr[i].w[2 * u], false), cvt2(kr[i].w[2 * u], true), cvt2(kr[i].w[2 * u + 1], false),
-                      cvt2(kr[i].w[2 * u + 1], true)};
-        } else {
-          *reinterpret_cast<uint4*>(lds + key_at<D>(key, cc)) = uint4{kr[i].w[0], kr[i].w[1], kr[i].w[2], kr[i].w[3]};
+      for (int i = 0; i < KL; ++i) {
+        const uint8_t* p = st.v + off + (int64_t)(KI * i) * st.slot_stride;
+        if constexpr (F8) vr[i] = load_words<4>(p + vo);
+        else to_lds(p, vo, at + i * 1024);
+      }
+    }
+    // e4m3: the codes that were loaded, converted
+    static __device__ __forceinline__ void store(const Words<4>& w, uint8_t* row, int cc, int swizzle) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<uint4*>(row + (((2 * cc + u) ^ swizzle) * 16)) =
+            uint4{cvt2(w.w[2 * u], false), cvt2(w.w[2 * u], true), cvt2(w.w[2 * u + 1], false), cvt2(w.w[2 * u + 1], true)};
+    }
+    __device__ __forceinline__ void store_k(uint8_t* lds) {
+      if constexpr (F8) {
+#pragma unroll
+        for (int i = 0; i < KL; ++i) {
+          const int lane = threadIdx.x & 63, key = lane / KP + KI * i;
+          store(kr[i], lds + (16 * wave + key) * (D * 2), lane % KP, key_swizzle<D>(key));
         }
       }
     }
-    // transposed; k: the tile's first key
-    __device__ __forceinline__ void store_v(uint8_t* lds, uint32_t* odd, int k, int blo, int bup) {
-      const int lane = threadIdx.x & 63, g = lane >> 5;
-      constexpr int NW = VW ? VW : 1;
-      if (k + kTile > blo) {
-        // values that no row of the block sees count as zero, and so do, for
-        // now, those that are not finite
-        uint32_t any = 0;
+    __device__ __forceinline__ void store_v(uint8_t* lds) {
+      if constexpr (F8) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const bool dead = k + 16 * wave + 4 * g + (e & 3) + 8 * (e >> 2) >= bup;
-            const uint32_t v = dead ? 0u : vr[e].w[w], bad = not_finite<F8>(v);
-            vr[e].w[w] = only_finite<F8>(v, bad);
-            any |= bad;
-          }
-        const bool found = __builtin_amdgcn_ballot_w64(any != 0) != 0;
-        if (lane == 0) odd[wave] = found;
+        for (int i = 0; i < KL; ++i) {
+          const int lane = threadIdx.x & 63, key = lane / KP + KI * i;
+          store(vr[i], lds + (16 * wave + key) * (D * 2), lane % KP, value_swizzle<D>(key));
+        }
       }
-      uint32_t x[8][DW / 2];
+    }
+    // The tile at k, if it has masks: values that no row of the block sees
+    // count as zero (the slots may hold anything), and so do, for now, those
+    // that are not finite.  The wave's own 16 keys, once they are in LDS.
+    __device__ __forceinline__ void mend_v(uint8_t* lds, uint32_t* odd, int k, int blo, int bup) {
+      if (k + kTile <= blo) return;
+      const int lane = threadIdx.x & 63;
+      if constexpr (F8) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (one wave wrote, other lanes read)
+      uint32_t any = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+      for (int i = 0; i < D / 32; ++i) {
+        uint4* p = reinterpret_cast<uint4*>(lds + (wave * (D / 32) + i) * 1024 + lane * 16);
+        const bool dead = k + 16 * wave + (i * 64 + lane) / (D / 8) >= bup;
+        const uint4 u = *p;
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int w = 0; w < DW / 2; ++w) x[e][w] = F8 ? cvt2(vr[e].w[0], w & 1) : vr[e].w[w];
-#pragma unroll
-      for (int j = 0; j < DW; ++j) {
-        const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-        *reinterpret_cast<uint4*>(lds + value_at<D>(DW * (lane & 31) + j, 2 * wave + g)) =
-            uint4{__builtin_amdgcn_perm(x[1][j >> 1], x[0][j >> 1], sel), __builtin_amdgcn_perm(x[3][j >> 1], x[2][j >> 1], sel),
-                  __builtin_amdgcn_perm(x[5][j >> 1], x[4][j >> 1], sel), __builtin_amdgcn_perm(x[7][j >> 1], x[6][j >> 1], sel)};
+        for (int j = 0; j < 4; ++j) {
+          w[j] = dead ? 0u : w[j];
+          const uint32_t bad = not_finite<false>(w[j]);
+          w[j] = only_finite<false>(w[j], bad);
+          any |= bad;
+        }
+        *p = uint4{w[0], w[1], w[2], w[3]};
       }
+      const bool found = __builtin_amdgcn_ballot_w64(any != 0) != 0;
+      if (lane == 0) odd[wave] = found;
     }
   };
 
@@ -212,39 +247,52 @@ struct Tiles {
                                        int bup, float c, const int* ko, const int* vo, TilesLds<D>& sh) {
     const bool more = k + kTile < k1;
     const int mid = k + kTile / 2;
-    if (more) g.load_v(st);
+    constexpr int kHalf = kTile / 2 * D * 2;   // bytes of 32 keys
+    float t;
+    if (more) g.load_v(st, g.v_at(sh, B ^ 1));
     if (k < up) {
-      step(s, sh.k[B] + kTile / 2 * D * 2, sh.v[B], c, ko, vo);
+      step(s, t, sh.k[B] + kHalf, sh.v[B], c, ko, vo);
       unfinite(st, k, k, up, blo, sh.odd[B]);
-      if (mid < up) prepare(s, mid, lo, c);
+      if (mid < up) prepare(s, t, mid, lo, c);
     }
     if (more) {
-      g.store_k(sh.k[B ^ 1]);
-      __syncthreads();
-      if (k + 2 * kTile < k1) g.load_k(st, k + 2 * kTile, k1);
+      if constexpr (F8) g.store_k(sh.k[B ^ 1]);
+      else wait_loads<KL>();   // the keys; the values are younger
+      wait_lds_barrier();
+      if (k + 2 * kTile < k1) g.load_k(st, k + 2 * kTile, k1, g.k_at(sh, B));
     }
     if (mid < up) {
-      step(s, sh.k[B ^ 1], sh.v[B], c, ko, vo + 2);   // (the scores of a tile that is not there are not used)
+      step(s, t, sh.k[B ^ 1], sh.v[B] + kHalf, c, ko, vo);   // (the scores of a tile that is not there are not used)
       unfinite(st, mid, k, up, blo, sh.odd[B]);
-      if (more && k + kTile < up) prepare(s, k + kTile, lo, c);
+      if (more && k + kTile < up) prepare(s, t, k + kTile, lo, c);
     }
     if (more) {
-      g.store_v(sh.v[B ^ 1], sh.odd[B ^ 1], k + kTile, blo, bup);
-      __syncthreads();
+      if constexpr (F8) g.store_v(sh.v[B ^ 1]);
+      else if (k + 2 * kTile < k1) wait_loads<KL>();   // the values; the next keys are younger
+      else wait_loads<0>();
+      g.mend_v(sh.v[B ^ 1], sh.odd[B ^ 1], k + kTile, blo, bup);
+      wait_lds_barrier();
     }
   }
 
-  // Scores of the 32 keys at k: masks, and the running maximum.
-  __device__ __forceinline__ void prepare(f32x16& s, int k, int lo, float c) {
+  // The largest of 16 scores of the lane's row.
+  static __device__ __forceinline__ float largest(const f32x16& s) {
+    float t = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t = fmaxf(t, s[i]);
+    return t;
+  }
+
+  // Scores of the 32 keys at k, the largest of them in t: masks, and the
+  // running maximum.
+  __device__ __forceinline__ void prepare(f32x16& s, float t, int k, int lo, float c) {
     if (k + kTile / 2 > lo) {
       const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = k + 8 * (i >> 2) + 4 * g + (i & 3) < hi ? s[i] : -__builtin_inff();
+      t = largest(s);
     }
-    float top = s[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    top *= c;
+    float top = t * c;
     if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top);
@@ -258,9 +306,23 @@ struct Tiles {
     }
   }
 
-  // The weights of scores s and their values (pieces vo[0], vo[1] of v); s
-  // becomes the scores of the 32 keys at kn.
-  __device__ __forceinline__ void step(f32x16& s, const uint8_t* kn, const uint8_t* v, float c, const int* ko,
+  // 8 keys of element 32 d + l%32 (16-key group a of the half at v)
+  static __device__ __forceinline__ uint4 values(const uint8_t* v, int off, int a) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4 lds_t;
+    union {
+      s16x4 h[2];
+      uint4 u;
+    } r;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      r.h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t*)(v + off + (16 * a + 8 * e) * (D * 2)));
+    return r.u;
+  }
+
+  // The weights of scores s and their values (32 keys at v); s becomes the
+  // scores of the 32 keys at kn, t their largest.
+  __device__ __forceinline__ void step(f32x16& s, float& t, const uint8_t* kn, const uint8_t* v, float c, const int* ko,
                                        const int* vo) {
     const bf16x2 ones = __builtin_bit_cast(bf16x2, 0x3F803F80u);
     f32x16 sn;
@@ -280,8 +342,9 @@ struct Tiles {
     for (int a = 0; a < 2; ++a) {
       const uint4 pa = uint4{p[4 * a], p[4 * a + 1], p[4 * a + 2], p[4 * a + 3]};
 #pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] = mfma32(*reinterpret_cast<const uint4*>(v + vo[a] + d * kRegion), pa, o[d]);
+      for (int d = 0; d < DT; ++d) o[d] = mfma32(values(v, vo[d], a), pa, o[d]);
     }
+    t = largest(sn);
     s = sn;
   }
 

@@ -28,7 +28,7 @@ struct Out {
 };
 template <int D>
 __device__ __forceinline__ Out out_of(const AttnArgs& a, const Item& it, int row, int h, int slot) {
-  const int tok = row / a.gq, hh = row - tok * a.gq;
+  const int tok = a.gq_d.of(row), hh = row - tok * a.gq;
   Out o;
   o.at = ((int64_t)(it.t0 + tok) * a.hq + h * a.gq + hh) * (a.plan.sp + a.plan.so) + slot;
   o.y = a.y + (int64_t)(it.t0 + tok) * a.ys + (int64_t)(h * a.gq + hh) * D;
@@ -42,9 +42,9 @@ __device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, in
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
   Keys<D, F8> R;
   R.start(a, it, row0, h, flip);
-  const Stream st = stream_of(a, h, it.table, it.len);
+  const Stream st = stream_of(a, h, it);
   const int last = min(row0 + 16, it.rows) - 1;
-  const int lo = it.sees(row0 / a.gq), up = it.sees(last / a.gq);
+  const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(last));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int quarter = ((c1 - c0 + 32 * kWaves - 1) / (32 * kWaves)) * 32;
   const int w0 = c0 + wave * quarter, w1 = min(c1, w0 + quarter);
@@ -64,27 +64,46 @@ __device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, in
   });
 }
 
-// The lane's row of a wave's tile of results, to the output or the workspace.
+// A wave's tile of results, to the output or the workspace.  The output goes
+// through the wave's part of LDS (the walk is over), so that 16 bytes a lane
+// cover whole rows.
 template <int D, bool F8>
 __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, const Tiles<D, F8>& R, int row0, int h,
-                                          int slot, float vs) {
-  const int lane = threadIdx.x & 63, g = lane >> 5, row = row0 + (lane & 31);
+                                          int slot, float vs, TilesLds<D>& sh) {
+  const int lane = threadIdx.x & 63, g = lane >> 5, i32 = lane & 31;
   const float l = R.l + __shfl_xor(R.l, 32);
+  if (a.plan.direct) {
+    constexpr int kRow = D * 2 + 16;   // of LDS: neighbouring rows in other banks
+    static_assert(kWaves * kTileRows * kRow <= (int)sizeof(sh.k) + (int)sizeof(sh.v), "the rows fit over the tiles");
+    uint8_t* mine = &sh.k[0][0] + (threadIdx.x >> 6) * (kTileRows * kRow);
+    const float f = l == 0.f ? 0.f : vs / l;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x[4] = {R.o[d][4 * i], R.o[d][4 * i + 1], R.o[d][4 * i + 2], R.o[d][4 * i + 3]};
+        store_y<4>(reinterpret_cast<uint16_t*>(mine + i32 * kRow) + 32 * d + 8 * i + 4 * g, x, f);
+      }
+    constexpr int P = D / 8;   // pieces of a row
+#pragma unroll
+    for (int i = 0; i < kTileRows * P / 64; ++i) {
+      const int rr = (i * 64 + lane) / P, c = lane % P;
+      if (row0 + rr >= it.rows) continue;
+      const Out w = out_of<D>(a, it, row0 + rr, h, slot);
+      *reinterpret_cast<uint4*>(w.y + c * 8) = *reinterpret_cast<const uint4*>(mine + rr * kRow + c * 16);
+    }
+    return;
+  }
+  const int row = row0 + i32;
   if (row >= it.rows) return;
   const Out w = out_of<D>(a, it, row, h, slot);
-  const float f = a.plan.direct ? (l == 0.f ? 0.f : vs / l) : vs;
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x[4] = {R.o[d][4 * i], R.o[d][4 * i + 1], R.o[d][4 * i + 2], R.o[d][4 * i + 3]};
-      const int e = 32 * d + 8 * i + 4 * g;
-      if (a.plan.direct)
-        store_y<4>(w.y + e, x, f);
-      else
-        *reinterpret_cast<f32x4*>(a.po + w.at * D + e) = f32x4{x[0] * f, x[1] * f, x[2] * f, x[3] * f};
-    }
-  if (!a.plan.direct && g == 0) a.pml[2 * w.at] = R.m, a.pml[2 * w.at + 1] = l;
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<f32x4*>(a.po + w.at * D + 32 * d + 8 * i + 4 * g) =
+          f32x4{R.o[d][4 * i] * vs, R.o[d][4 * i + 1] * vs, R.o[d][4 * i + 2] * vs, R.o[d][4 * i + 3] * vs};
+  if (g == 0) a.pml[2 * w.at] = R.m, a.pml[2 * w.at + 1] = l;
 }
 
 // One walk of a block's rows over keys [c0, c1) of an item.
@@ -95,10 +114,10 @@ __device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, Ti
   const int row0 = blk0 + kTileRows * wave;
   const bool live = row0 < it.rows;
   const int blast = min(blk0 + kBlockRows, it.rows) - 1, wlast = min(row0 + kTileRows, it.rows) - 1;
-  const int blo = it.sees(blk0 / a.gq), bup = it.sees(blast / a.gq);
-  const int lo = it.sees(row0 / a.gq), up = it.sees(wlast / a.gq);
-  R.hi = it.sees(min(row0 + (int)(threadIdx.x & 31), it.rows - 1) / a.gq);
-  R.walk(stream_of(a, h, it.table, it.len), c0, c1, lo, up, blo, bup, c, live, sh);
+  const int blo = it.sees(a.gq_d.of(blk0)), bup = it.sees(a.gq_d.of(blast));
+  const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(max(wlast, 0)));
+  R.hi = it.sees(a.gq_d.of(min(row0 + (int)(threadIdx.x & 31), it.rows - 1)));
+  R.walk(stream_of(a, h, it), c0, c1, lo, up, blo, bup, c, live, sh);
 }
 
 template <int D, bool F8>
@@ -111,7 +130,7 @@ __device__ __forceinline__ void tiles_block(const AttnArgs& a, const Item& it, i
   R.clear();
   R.load_q(a, it, row0, h, flip);
   tiles_walk<D, F8>(a, it, R, blk0, h, c0, c1, c, sh);
-  put_tiles<D, F8>(a, it, R, row0, h, slot, vs);
+  put_tiles<D, F8>(a, it, R, row0, h, slot, vs, sh);
 }
 
 // Split form.  TO, TP: own keys, prefixes by Tiles (else by Keys).
@@ -125,11 +144,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int n
   const int blk = prefix ? blockIdx.x : blockIdx.x - npre;
   const int rb = prefix ? a.plan.rbp : a.plan.rbo, ns = prefix ? a.plan.sp : a.plan.so;
   const int chunk = prefix ? a.plan.cp : a.plan.co;
-  const int r = blk % rb;
-  int u = blk / rb;
-  const int h = u % a.kv.heads;
-  u /= a.kv.heads;
-  const int s = u % ns, b = u / ns;
+  int u = (prefix ? a.plan.rbp_d : a.plan.rbo_d).of(blk);
+  const int r = blk - u * rb;
+  const int u2 = a.hkv_d.of(u), h = u - u2 * a.kv.heads;
+  const int b = (prefix ? a.plan.sp_d : a.plan.so_d).of(u2), s = u2 - b * ns;
   const Item it = prefix ? prefix_item(a, b) : own_item(a, b);
   const bool tiles = prefix ? TP : TO;
   const int row0 = r * (tiles ? kBlockRows : Keys<D, F8>::kRows);
@@ -158,7 +176,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= (int64_t)a.n * a.hq) return;
-  const int tok = (int)(row / a.hq), h = (int)(row - (int64_t)tok * a.hq);
+  const int tok = a.hq_d.of((int)row), h = (int)row - tok * a.hq;
   const int sp = a.plan.sp, slots = sp + a.plan.so;
   const f32x2* ml = reinterpret_cast<const f32x2*>(a.pml) + row * slots;
   const float* po = a.po + row * slots * D + (lane % L) * 4;
@@ -230,15 +248,15 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 }
 
 // Long queries.  Blocks of one (sequence, kv head) follow each other on one
-// XCD, the longest rows first.
-template <int D, bool F8>
+// XCD, the longest rows first.  PRE: some sequences have a prefix.
+template <int D, bool F8, bool PRE>
 __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_rows(AttnArgs a) {
   __shared__ TilesLds<D> sh;
   const int xcd = blockIdx.x & 7, j8 = blockIdx.x >> 3;
-  const int rb = a.plan.rbo;
-  const int pair = (j8 / rb) * 8 + xcd, rblk = rb - 1 - j8 % rb;
+  const int p8 = a.plan.rbo_d.of(j8), rblk = a.plan.rbo - 1 - (j8 - p8 * a.plan.rbo);
+  const int pair = p8 * 8 + xcd;
   if (pair >= a.B * a.kv.heads) return;
-  const int b = pair / a.kv.heads, h = pair - b * a.kv.heads;
+  const int b = a.hkv_d.of(pair), h = pair - b * a.kv.heads;
   const Item own = own_item(a, b);
   const int blk0 = rblk * kBlockRows;
   if (blk0 >= own.rows) return;
@@ -248,18 +266,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_rows(AttnArgs a) {
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, own, row0, h, flip);
-  const int gr = group_of(a, b);
-#pragma unroll 1
-  for (int part = gr < 0 ? 1 : 0; part < 2; ++part) {
+  if constexpr (PRE) {   // the group's prefix, all of it
+    const int gr = group_of(a, b);
     Item it = own;
-    if (part == 0) {   // the prefix, all of it
-      it.len = clampi(a.p_len[gr], 0, a.max_pre);
-      it.table = a.p_pages + (int64_t)gr * a.ppw;
-      it.causal = false;
-    }
+    it.len = gr < 0 ? 0 : clampi(a.p_len[gr], 0, a.max_pre);
+    it.table = a.p_pages + (int64_t)max(gr, 0) * a.ppw;
+    it.width = a.ppw;
+    it.causal = false;
     tiles_walk<D, F8>(a, it, R, blk0, h, 0, it.len, c, sh);
   }
-  put_tiles<D, F8>(a, own, R, row0, h, 0, vs);
+  tiles_walk<D, F8>(a, own, R, blk0, h, 0, own.len, c, sh);
+  put_tiles<D, F8>(a, own, R, row0, h, 0, vs, sh);
 }
 
 template <int D, bool F8>
@@ -268,8 +285,10 @@ void go(const AttnArgs& a) {
   const AttnPlan& p = a.plan;
   const dim3 blk(64 * kWaves);
   if (p.rows) {
-    const unsigned pairs = (unsigned)(((int64_t)a.B * a.kv.heads + 7) / 8 * 8);
-    hipLaunchKernelGGL((k_attn_rows<D, F8>), dim3(pairs * p.rbo), blk, 0, st, a);
+    const int pairs8 = (int)(((int64_t)a.B * a.kv.heads + 7) / 8);
+    const dim3 g((unsigned)(8 * pairs8 * p.rbo));
+    if (a.G > 0) hipLaunchKernelGGL((k_attn_rows<D, F8, true>), g, blk, 0, st, a);
+    else hipLaunchKernelGGL((k_attn_rows<D, F8, false>), g, blk, 0, st, a);
     return;
   }
   const int npre = a.G * a.kv.heads * p.rbp * p.sp, nown = a.B * a.kv.heads * p.rbo * p.so;

@@ -96,6 +96,8 @@ int64_t blocks_of(const dc::AttnPlan& p, int64_t B, int64_t G, int64_t heads) {
 
 namespace dc {
 
+constexpr int64_t kOwnBlocks = 512, kPrefixBlocks = 512;
+
 AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, int32_t max_q, int32_t max_kv, int32_t G,
                    int32_t max_gq, int32_t max_pre) {
   AttnPlan p{};
@@ -115,9 +117,9 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   p.rbo = (int32_t)(p.to ? rb : (ro + 15) / 16);
   p.rbp = (int32_t)(p.tp ? (rg + 127) / 128 : (rg + 15) / 16);
   // as many ranges as fill the card twice, each of 128 keys (a step a wave) or more
-  auto split = [](int64_t items, int64_t keys, int32_t* s, int32_t* c) {
+  auto split = [](int64_t items, int64_t keys, int64_t want, int32_t* s, int32_t* c) {
     if (items < 1) items = 1;
-    int64_t n = (512 + items - 1) / items;
+    int64_t n = (want + items - 1) / items;
     const int64_t most = (keys + 127) / 128;
     if (n > most) n = most;
     if (n > 64) n = 64;
@@ -127,9 +129,9 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
     *c = (int32_t)ch;
     *s = (int32_t)((keys + ch - 1) / ch);
   };
-  split((int64_t)B * hkv * p.rbo, max_kv, &p.so, &p.co);
+  split((int64_t)B * hkv * p.rbo, max_kv, kOwnBlocks, &p.so, &p.co);
   p.cp = 64;
-  if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, &p.sp, &p.cp);
+  if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, kPrefixBlocks, &p.sp, &p.cp);
   if (p.sp == 0 && p.so <= 1) {
     p.so = 1;
     p.direct = true;
@@ -237,6 +239,13 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   a.scale = (float)((double)scale * 1.4426950408889634074);   // the kernels' exponentials are base 2
   a.hq = q_heads;
   a.gq = q_heads / kv->heads;
+  a.hq_d = dc::div_by(a.hq);
+  a.gq_d = dc::div_by(a.gq);
+  a.hkv_d = dc::div_by(kv->heads);
+  a.plan.rbo_d = dc::div_by(a.plan.rbo);
+  a.plan.rbp_d = dc::div_by(a.plan.rbp);
+  a.plan.so_d = dc::div_by(a.plan.so);
+  a.plan.sp_d = dc::div_by(a.plan.sp);
   a.n = N;
   a.dim = kv->dim;
   a.e4m3 = kv->dtype == DC_KV_E4M3;

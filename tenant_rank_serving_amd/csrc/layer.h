@@ -31,6 +31,23 @@ struct AppendArgs {
 };
 int launch_append(const AppendArgs& a);
 
+// n / d for 0 <= n < 2^31 with one multiplication: floor(n M / 2^(32+s)) with
+// M = ceil(2^(32+s) / d) and 2^s < d <= 2^(s+1) (M < 2^32; exact for 31 bits).
+struct Div {
+  uint32_t m;
+  int32_t s, d;
+#if defined(__HIPCC__)
+  __device__ __forceinline__ int32_t of(int32_t n) const { return d == 1 ? n : (int32_t)(__umulhi((uint32_t)n, m) >> s); }
+#endif
+};
+inline Div div_by(int32_t d) {
+  Div r{0, 0, d < 1 ? 1 : d};
+  if (r.d == 1) return r;
+  while ((INT64_C(2) << r.s) < r.d) ++r.s;
+  r.m = (uint32_t)(((UINT64_C(1) << (32 + r.s)) + (uint64_t)r.d - 1) / (uint64_t)r.d);
+  return r;
+}
+
 // How one attention call is split, from the host's bounds alone (the lengths
 // stay on the device).
 struct AttnPlan {
@@ -40,6 +57,7 @@ struct AttnPlan {
   int32_t so, sp;     // key splits of a sequence's own keys / of a prefix
   int32_t co, cp;     // keys of a split (multiples of 64)
   bool direct;        // one split in all: the outputs are written at once
+  Div rbo_d, rbp_d, so_d, sp_d;
   size_t o_off, ws;   // split form: partial sums at o_off of the workspace, its size
 };
 
@@ -51,6 +69,7 @@ struct AttnArgs {
   int64_t qs, ys;     // row strides, elements
   float scale;        // times log2(e)
   int32_t hq, gq, n, dim, e4m3;
+  Div hq_d, gq_d, hkv_d;
   int32_t B, max_q, max_kv, pw;
   const int32_t *q_start, *kv_len, *pages;
   int32_t G, max_gq, max_pre, ppw;
