@@ -175,19 +175,45 @@ __global__ void __launch_bounds__(256) k_w4_pack(const uint16_t* __restrict__ W,
 
 __global__ void k_w4_flag(uint32_t* flag) { *flag = 0; }
 
-template <int RT, int TT, int NW, int U>
+template <int RT, int TT, int U = 1>
 void go(const W4Args& a) {
-  const dim3 g((unsigned)((a.out + RT * 16 - 1) / (RT * 16)), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
-  hipLaunchKernelGGL((k_w4<RT, TT, NW, U>), g, dim3(64 * NW), 0, reinterpret_cast<hipStream_t>(a.stream), a.w, a.x, a.y,
+  const dim3 g((unsigned)((a.out / 16 + RT - 1) / RT), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
+  hipLaunchKernelGGL((k_w4<RT, TT, 8, U>), g, dim3(512), 0, reinterpret_cast<hipStream_t>(a.stream), a.w, a.x, a.y,
                      a.out, a.in, a.T);
 }
 
 }  // namespace
 
+// The tile of a block.  A CU reads about 17 bytes a nanosecond through its L1
+// when all read (x comes from L2 again in every block), so the time is that
+// of what the fullest CU reads: RT row tiles of the matrix (8.5 bytes an
+// input with the scales) and the tokens' x (2 bytes an input each), for each
+// round of 256 blocks.  Measured, us, all 10 tiles timed: 4096 x 4096 with 64 tokens (1,1) 18.6,
+// (1,4) 17.1, (4,1) 8.8; 11008 x 4096 with 16 (1,1) 14.7, (2,1) 11.6, (3,1)
+// 8.2, (4,1) 9.0, with 64 (4,4) 21.5, (3,4) 20.3, (6,2) 15.6; 4096 x 14336
+// with 1 (1,1) 10.3, (2,1) 12.6.
 int launch_w4(const W4Args& a) {
-  if (a.T <= 16) go<1, 1, 8, 4>(a);
-  else if (a.T <= 32) go<2, 2, 8, 2>(a);
-  else go<4, 4, 8, 1>(a);
+  constexpr int kTiles[][2] = {{1, 1}, {2, 1}, {3, 1}, {4, 1}, {6, 1}, {8, 1}, {2, 2}, {4, 2}, {6, 2}, {8, 2}};
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int c = 0; c < 10; ++c) {
+    const int64_t rt = kTiles[c][0], tok = 16 * kTiles[c][1];
+    const int64_t blocks = (a.out / 16 + rt - 1) / rt * ((a.T + tok - 1) / tok);
+    const int64_t cost = (blocks + 255) / 256 * (17 * rt + 4 * (a.T < tok ? a.T : tok));
+    if (cost < least) least = cost, best = c;
+  }
+  switch (best) {
+    case 0: go<1, 1, 4>(a); break;
+    case 1: go<2, 1>(a); break;
+    case 2: go<3, 1>(a); break;
+    case 3: go<4, 1>(a); break;
+    case 4: go<6, 1>(a); break;
+    case 5: go<8, 1>(a); break;
+    case 6: go<2, 2>(a); break;
+    case 7: go<4, 2>(a); break;
+    case 8: go<6, 2>(a); break;
+    default: go<8, 2>(a); break;
+  }
   return (int)hipGetLastError();
 }
 
