@@ -69,18 +69,41 @@ struct Stream {
   int32_t shift;            // log2 of a page's slots
 };
 
+// Of a kv head; a sequence's own keys or a group's prefix.
+__device__ __forceinline__ Stream stream_of(const AttnArgs& a, int h, const int32_t* table, int width) {
+  Stream st;
+  st.k = a.kv.k + h * a.kv.head_stride;
+  st.v = a.kv.v + h * a.kv.head_stride;
+  st.page_stride = a.kv.page_stride;
+  st.slot_stride = (int)a.kv.slot_stride;
+  st.table = table;
+  st.width = width;
+  st.shift = a.kv.shift;
+  st.num_pages = a.kv.num_pages;
+  return st;
+}
+
+__device__ __forceinline__ Stream own_stream(const AttnArgs& a, int h, int b) {
+  return stream_of(a, h, a.pages + (int64_t)b * a.pw, a.pw);
+}
+__device__ __forceinline__ Stream prefix_stream(const AttnArgs& a, int h, int g) {
+  return stream_of(a, h, a.p_pages + (int64_t)g * a.ppw, a.ppw);
+}
+
 // A stream's page numbers, 64 of them in a register, one a lane.
 struct Pages {
   int base, pg;
   __device__ __forceinline__ void fill(const Stream& st, int p) {
     base = p;
+    pg = 0;
+    if (st.width == 0) return;   // a call without keys may come without a table
     pg = st.table[min(p + (int)(threadIdx.x & 63), st.width - 1)];
     pg = (unsigned)pg < (unsigned)st.num_pages ? pg : 0;   // never outside the cache
   }
   // Byte offset of key `at` (the first of 16 that share a page); ascending.
   __device__ __forceinline__ int64_t offset(const Stream& st, int at) {
     const int p = at >> st.shift;
-    if (p - base >= 64) fill(st, p);
+    if (__builtin_expect(p - base >= 64, 0)) fill(st, p);
     const int64_t page = __builtin_amdgcn_readlane(pg, p - base);
     return page * st.page_stride + (int64_t)(at & ((1 << st.shift) - 1)) * st.slot_stride;
   }
@@ -110,24 +133,9 @@ struct Item {
   int32_t len;            // keys
   int32_t first;          // own keys: token j sees first + j + 1 of them
   bool causal;
-  const int32_t* table;
-  int32_t width;
   // keys that token tok sees
   __device__ __forceinline__ int sees(int tok) const { return causal ? clampi(first + tok + 1, 0, len) : len; }
 };
-
-__device__ __forceinline__ Stream stream_of(const AttnArgs& a, int h, const Item& it) {
-  Stream st;
-  st.k = a.kv.k + h * a.kv.head_stride;
-  st.v = a.kv.v + h * a.kv.head_stride;
-  st.page_stride = a.kv.page_stride;
-  st.slot_stride = (int)a.kv.slot_stride;
-  st.table = it.table;
-  st.width = it.width;
-  st.shift = a.kv.shift;
-  st.num_pages = a.kv.num_pages;
-  return st;
-}
 
 // Sequence b with its own keys; what the bounds do not cover is cut.
 __device__ __forceinline__ Item own_item(const AttnArgs& a, int b) {
@@ -139,8 +147,6 @@ __device__ __forceinline__ Item own_item(const AttnArgs& a, int b) {
   it.len = clampi(a.kv_len[b], 0, a.max_kv);
   it.first = it.len - it.nt;
   it.causal = true;
-  it.table = a.pages + (int64_t)b * a.pw;
-  it.width = a.pw;
   return it;
 }
 // The tokens of group g's sequences with its prefix.
@@ -154,8 +160,6 @@ __device__ __forceinline__ Item prefix_item(const AttnArgs& a, int g) {
   it.len = clampi(a.p_len[g], 0, a.max_pre);
   it.first = 0;
   it.causal = false;
-  it.table = a.p_pages + (int64_t)g * a.ppw;
-  it.width = a.ppw;
   return it;
 }
 

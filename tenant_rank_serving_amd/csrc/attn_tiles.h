@@ -1,4 +1,4 @@
-// The walk for more than 16 query rows: a block takes 128 rows, wave w rows
+// The walk for more than 32 query rows: a block takes 128 rows, wave w rows
 // 32w .. 32w+31, and its keys come through LDS in tiles of 64 that all waves
 // share.  Included inside namespace dc, anonymous namespace, of k_attn.hip,
 // behind attn_common.h.
@@ -73,9 +73,10 @@ struct Tiles {
     }
   }
 
-  // Keys [k0, k1) of the stream (k0 a multiple of 64) for the block; a wave
-  // without rows (live = false) only carries tiles.  The wave's rows all see
-  // the keys below lo and none see those from up on; blo, bup: the block's.
+  // Keys [k0, k1) of the stream (k0 a multiple of 64, its page in `pages`) for
+  // the block; a wave without rows (live = false) only carries tiles.  The
+  // wave's rows all see the keys below lo and none see those from up on; blo,
+  // bup: the block's.
   //
   // Half tiles of 32 keys: step h multiplies the keys of half h + 1, takes the
   // exponentials of half h and multiplies its values, in one stretch of code
@@ -84,11 +85,15 @@ struct Tiles {
   // K of the next tile is needed in a tile's second step and V in the next
   // tile's first; each is on its way for two steps.  With two buffers, one
   // barrier a step.
-  __device__ __forceinline__ void walk(const Stream& st, int k0, int k1, int lo, int up, int blo, int bup, float c,
-                                       bool live, TilesLds<D>& sh) {
+  __device__ __forceinline__ void walk(const Stream& st, const Pages& pages, int k0, int k1, int lo, int up, int blo,
+                                       int bup, float c, bool live, TilesLds<D>& sh) {
     k1 = min(k1, bup);
     if (k0 >= k1) return;
-    Stage g(st, sh);
+    // Q is here before the first keys leave: a wait for it inside the loop
+    // would be one for them too (loads return in order; 8x2048 prompt: 187 us, 210 with it).
+#pragma unroll
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
+    Stage g(st, pages, sh);
     const int lane = threadIdx.x & 63, half = lane >> 5, i32 = lane & 31;
     int ko[KS], vo[DT];
 #pragma unroll
@@ -144,10 +149,9 @@ struct Tiles {
     Pages pages;
     int64_t off;
     int wave, ko[F8 ? 1 : KL], vo;   // the lane's offsets in 16 keys' rows
-    __device__ __forceinline__ Stage(const Stream& st, const TilesLds<D>& sh) {
+    __device__ __forceinline__ Stage(const Stream& st, const Pages& p, const TilesLds<D>& sh) : pages(p) {
       const int lane = threadIdx.x & 63;
       wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-      pages.base = -64;
       base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)&sh.k[0][0] + wave * (16 * D * 2);
       const int key = lane / KP, pos = lane % KP;   // LDS takes 16 bytes a lane, in the order of the lanes
       if constexpr (F8) {
@@ -217,7 +221,7 @@ struct Tiles {
     // count as zero (the slots may hold anything), and so do, for now, those
     // that are not finite.  The wave's own 16 keys, once they are in LDS.
     __device__ __forceinline__ void mend_v(uint8_t* lds, uint32_t* odd, int k, int blo, int bup) {
-      if (k + kTile <= blo) return;
+      if (__builtin_expect(k + kTile <= blo, 1)) return;
       const int lane = threadIdx.x & 63;
       if constexpr (F8) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (one wave wrote, other lanes read)
       uint32_t any = 0;
@@ -249,24 +253,24 @@ struct Tiles {
     const int mid = k + kTile / 2;
     constexpr int kHalf = kTile / 2 * D * 2;   // bytes of 32 keys
     float t;
-    if (more) g.load_v(st, g.v_at(sh, B ^ 1));
-    if (k < up) {
+    if (__builtin_expect(more, 1)) g.load_v(st, g.v_at(sh, B ^ 1));
+    if (__builtin_expect(k < up, 1)) {
       step(s, t, sh.k[B] + kHalf, sh.v[B], c, ko, vo);
       unfinite(st, k, k, up, blo, sh.odd[B]);
-      if (mid < up) prepare(s, t, mid, lo, c);
+      if (__builtin_expect(mid < up, 1)) prepare(s, t, mid, lo, c);
     }
-    if (more) {
+    if (__builtin_expect(more, 1)) {
       if constexpr (F8) g.store_k(sh.k[B ^ 1]);
       else wait_loads<KL>();   // the keys; the values are younger
       wait_lds_barrier();
-      if (k + 2 * kTile < k1) g.load_k(st, k + 2 * kTile, k1, g.k_at(sh, B));
+      if (__builtin_expect(k + 2 * kTile < k1, 1)) g.load_k(st, k + 2 * kTile, k1, g.k_at(sh, B));
     }
-    if (mid < up) {
+    if (__builtin_expect(mid < up, 1)) {
       step(s, t, sh.k[B ^ 1], sh.v[B] + kHalf, c, ko, vo);   // (the scores of a tile that is not there are not used)
       unfinite(st, mid, k, up, blo, sh.odd[B]);
-      if (more && k + kTile < up) prepare(s, t, k + kTile, lo, c);
+      if (__builtin_expect(more && k + kTile < up, 1)) prepare(s, t, k + kTile, lo, c);
     }
-    if (more) {
+    if (__builtin_expect(more, 1)) {
       if constexpr (F8) g.store_v(sh.v[B ^ 1]);
       else if (k + 2 * kTile < k1) wait_loads<KL>();   // the values; the next keys are younger
       else wait_loads<0>();
@@ -286,14 +290,14 @@ struct Tiles {
   // Scores of the 32 keys at k, the largest of them in t: masks, and the
   // running maximum.
   __device__ __forceinline__ void prepare(f32x16& s, float t, int k, int lo, float c) {
-    if (k + kTile / 2 > lo) {
+    if (__builtin_expect(k + kTile / 2 > lo, 0)) {
       const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = k + 8 * (i >> 2) + 4 * g + (i & 3) < hi ? s[i] : -__builtin_inff();
       t = largest(s);
     }
     float top = t * c;
-    if (__builtin_amdgcn_ballot_w64(top > m + kSlack)) {
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(top > m + kSlack) != 0, 0)) {
       top = fmaxf(top, __shfl_xor(top, 32));
       const float mn = fmaxf(m, top);
       const float f = __builtin_amdgcn_exp2f(m - mn);
@@ -350,7 +354,8 @@ struct Tiles {
 
   // See unfinite_pair: keys [k, k + 32) of the tile at k0.
   __device__ __forceinline__ void unfinite(const Stream& st, int k, int k0, int up, int blo, const uint32_t* odd) {
-    if (k0 + kTile <= blo || !(odd[0] | odd[1] | odd[2] | odd[3])) return;
+    if (__builtin_expect(k0 + kTile <= blo, 1)) return;
+    if (__builtin_expect(!(odd[0] | odd[1] | odd[2] | odd[3]), 1)) return;
     const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll 1
     for (int key = k; key < min(k + kTile / 2, up); ++key) {

@@ -1,7 +1,7 @@
 // Attention over the paged cache: y = sum_k softmax_k(scale q.k) v_k for
 // ragged sequences whose groups share prefixes.
 //
-// Two walks over keys: Keys (attn_keys.h) for at most 16 query rows of a kv
+// Two walks over keys: Keys (attn_keys.h) for at most 32 query rows of a kv
 // head, where the time is that of reading the cache, and Tiles (attn_tiles.h)
 // for more.  Two forms of a call, chosen from the host's bounds (attn_plan):
 //   split   a block takes the rows of one (sequence, kv head) or, for a
@@ -35,22 +35,26 @@ __device__ __forceinline__ Out out_of(const AttnArgs& a, const Item& it, int row
   return o;
 }
 
-template <int D, bool F8>
-__device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, int row0, int h, int c0, int c1, int slot,
-                                           KeysLds<D>& sh) {
+template <int D, bool F8, int N>
+__device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, const Stream& st, Pages& pages, int row0, int h,
+                                           int c0, int c1, int slot, KeysLds<D>& sh) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int last = min(row0 + 16 * N, it.rows) - 1;
+  const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(last));
+  const int w0 = c0 + 32 * wave, w1 = min(c1, up);
+  typename Keys<D, F8, N>::Stage g;
+  if (w0 < w1) {   // the first keys and values go first
+    g.seek(st, pages, w0, w1);
+    g.load_k(st);
+    g.load_v(st);
+  }
   uint32_t flip;
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
-  Keys<D, F8> R;
+  Keys<D, F8, N> R;
   R.start(a, it, row0, h, flip);
-  const Stream st = stream_of(a, h, it);
-  const int last = min(row0 + 16, it.rows) - 1;
-  const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(last));
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int quarter = ((c1 - c0 + 32 * kWaves - 1) / (32 * kWaves)) * 32;
-  const int w0 = c0 + wave * quarter, w1 = min(c1, w0 + quarter);
-  if (w0 < w1) R.walk(st, w0, w1, lo, up, c);
+  R.walk(st, g, pages, w0, w1, lo, up, c);
   constexpr int J = D / 16;
-  join<D, F8>(R, sh, [&](int row, int e, float m, float l, const float* x) __attribute__((always_inline)) {
+  join<D, F8, N>(R, sh, [&](int row, int e, float m, float l, const float* x) __attribute__((always_inline)) {
     if (row0 + row >= it.rows) return;
     const Out w = out_of<D>(a, it, row0 + row, h, slot);
     if (a.plan.direct) {
@@ -108,7 +112,8 @@ __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, con
 
 // One walk of a block's rows over keys [c0, c1) of an item.
 template <int D, bool F8>
-__device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, Tiles<D, F8>& R, int blk0, int h, int c0,
+__device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages,
+                                           Tiles<D, F8>& R, int blk0, int h, int c0,
                                            int c1, float c, TilesLds<D>& sh) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row0 = blk0 + kTileRows * wave;
@@ -117,28 +122,30 @@ __device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, Ti
   const int blo = it.sees(a.gq_d.of(blk0)), bup = it.sees(a.gq_d.of(blast));
   const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(max(wlast, 0)));
   R.hi = it.sees(a.gq_d.of(min(row0 + (int)(threadIdx.x & 31), it.rows - 1)));
-  R.walk(stream_of(a, h, it), c0, c1, lo, up, blo, bup, c, live, sh);
+  R.walk(st, pages, c0, c1, lo, up, blo, bup, c, live, sh);
 }
 
 template <int D, bool F8>
-__device__ __forceinline__ void tiles_block(const AttnArgs& a, const Item& it, int blk0, int h, int c0, int c1, int slot,
-                                            TilesLds<D>& sh) {
+__device__ __forceinline__ void tiles_block(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages, int blk0,
+                                            int h, int c0, int c1, int slot, TilesLds<D>& sh) {
   uint32_t flip;
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
   const int row0 = blk0 + kTileRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, it, row0, h, flip);
-  tiles_walk<D, F8>(a, it, R, blk0, h, c0, c1, c, sh);
+  tiles_walk<D, F8>(a, it, st, pages, R, blk0, h, c0, c1, c, sh);
   put_tiles<D, F8>(a, it, R, row0, h, slot, vs, sh);
 }
 
-// Split form.  TO, TP: own keys, prefixes by Tiles (else by Keys).
-template <int D, bool F8, bool TO, bool TP>
+// Split form.  WO, WP: how own keys and prefixes are walked, by Keys of 16 or
+// 32 rows (1, 2) or by Tiles (3).
+constexpr int kByTiles = 3;
+template <int D, bool F8, int WO, int WP>
 __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int npre) {
   __shared__ union {
     KeysLds<D> keys;
-    TilesLds<TO || TP ? D : 8> tiles;
+    TilesLds<WO == kByTiles || WP == kByTiles ? D : 8> tiles;
   } sh;
   const bool prefix = (int)blockIdx.x < npre;
   const int blk = prefix ? blockIdx.x : blockIdx.x - npre;
@@ -148,20 +155,29 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int n
   const int r = blk - u * rb;
   const int u2 = a.hkv_d.of(u), h = u - u2 * a.kv.heads;
   const int b = (prefix ? a.plan.sp_d : a.plan.so_d).of(u2), s = u2 - b * ns;
+  const int c0 = s * chunk;
+  // the page numbers are on their way while the lengths are read
+  const Stream st = prefix ? prefix_stream(a, h, b) : own_stream(a, h, b);
+  Pages pages;
+  pages.fill(st, c0 >> st.shift);
   const Item it = prefix ? prefix_item(a, b) : own_item(a, b);
-  const bool tiles = prefix ? TP : TO;
-  const int row0 = r * (tiles ? kBlockRows : Keys<D, F8>::kRows);
+  const int how = prefix ? WP : WO;
+  const int row0 = r * (how == kByTiles ? kBlockRows : 16 * how);
   if (row0 >= it.rows) return;
-  const int c0 = s * chunk, c1 = min(it.len, c0 + chunk);
+  const int c1 = min(it.len, c0 + chunk);
   if (c0 >= c1 && !a.plan.direct) return;   // the join knows that it holds nothing
   const int slot = prefix ? s : a.plan.sp + s;
-  if constexpr (TO || TP) {
-    if (tiles) {
-      tiles_block<D, F8>(a, it, row0, h, c0, c1, slot, sh.tiles);
-      return;
-    }
+#define DC_WALK(W_)                                                                                 \
+  if constexpr (W_ == kByTiles) tiles_block<D, F8>(a, it, st, pages, row0, h, c0, c1, slot, sh.tiles); \
+  else keys_block<D, F8, W_>(a, it, st, pages, row0, h, c0, c1, slot, sh.keys);
+  if constexpr (WO == WP) {
+    DC_WALK(WO)
+  } else if (prefix) {
+    DC_WALK(WP)
+  } else {
+    DC_WALK(WO)
   }
-  if constexpr (!TO || !TP) keys_block<D, F8>(a, it, row0, h, c0, c1, slot, sh.keys);
+#undef DC_WALK
 }
 
 // Joins the splits of a row: one wave a row.  Everything that does not depend
@@ -266,16 +282,19 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_rows(AttnArgs a) {
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, own, row0, h, flip);
+  Pages pages;
   if constexpr (PRE) {   // the group's prefix, all of it
     const int gr = group_of(a, b);
     Item it = own;
     it.len = gr < 0 ? 0 : clampi(a.p_len[gr], 0, a.max_pre);
-    it.table = a.p_pages + (int64_t)max(gr, 0) * a.ppw;
-    it.width = a.ppw;
     it.causal = false;
-    tiles_walk<D, F8>(a, it, R, blk0, h, 0, it.len, c, sh);
+    const Stream st = prefix_stream(a, h, max(gr, 0));
+    pages.fill(st, 0);
+    tiles_walk<D, F8>(a, it, st, pages, R, blk0, h, 0, it.len, c, sh);
   }
-  tiles_walk<D, F8>(a, own, R, blk0, h, 0, own.len, c, sh);
+  const Stream st = own_stream(a, h, b);
+  pages.fill(st, 0);
+  tiles_walk<D, F8>(a, own, st, pages, R, blk0, h, 0, own.len, c, sh);
   put_tiles<D, F8>(a, own, R, row0, h, 0, vs, sh);
 }
 
@@ -293,9 +312,16 @@ void go(const AttnArgs& a) {
   }
   const int npre = a.G * a.kv.heads * p.rbp * p.sp, nown = a.B * a.kv.heads * p.rbo * p.so;
   const dim3 g((unsigned)(npre + nown));
-  if (p.to) hipLaunchKernelGGL((k_attn_split<D, F8, true, true>), g, blk, 0, st, a, npre);
-  else if (p.tp) hipLaunchKernelGGL((k_attn_split<D, F8, false, true>), g, blk, 0, st, a, npre);
-  else hipLaunchKernelGGL((k_attn_split<D, F8, false, false>), g, blk, 0, st, a, npre);
+#define DC_SPLIT(WO_, WP_) hipLaunchKernelGGL((k_attn_split<D, F8, WO_, WP_>), g, blk, 0, st, a, npre)
+  switch (p.wo * 4 + p.wp) {
+    case 5: DC_SPLIT(1, 1); break;
+    case 6: DC_SPLIT(1, 2); break;
+    case 7: DC_SPLIT(1, 3); break;
+    case 10: DC_SPLIT(2, 2); break;
+    case 11: DC_SPLIT(2, 3); break;
+    default: DC_SPLIT(3, 3); break;
+  }
+#undef DC_SPLIT
   if (!p.direct)
     hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)(((int64_t)a.n * a.hq + 3) / 4)), dim3(256), 0, st, a);
 }

@@ -108,14 +108,16 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   if (ro > 32 && (int64_t)B * hkv * rb >= 256) {
     p.rows = true;
     p.rbo = (int32_t)rb;
-    p.co = p.cp = 64;
+    p.co = p.cp = 128;
     p.direct = true;
     return p;
   }
-  p.to = ro > 16;
-  p.tp = p.to || rg > 16;
-  p.rbo = (int32_t)(p.to ? rb : (ro + 15) / 16);
-  p.rbp = (int32_t)(p.tp ? (rg + 127) / 128 : (rg + 15) / 16);
+  auto walk = [](int64_t rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 3); };
+  p.wo = walk(ro);
+  p.wp = walk(rg) > p.wo ? walk(rg) : p.wo;
+  auto blocks = [](int64_t rows, int32_t how) { return (int32_t)(how == 3 ? (rows + 127) / 128 : (rows + 16 * how - 1) / (16 * how)); };
+  p.rbo = blocks(ro, p.wo);
+  p.rbp = blocks(rg, p.wp);
   // as many ranges as fill the card twice, each of 128 keys (a step a wave) or more
   auto split = [](int64_t items, int64_t keys, int64_t want, int32_t* s, int32_t* c) {
     if (items < 1) items = 1;
@@ -124,13 +126,13 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
     if (n > most) n = most;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
-    int64_t ch = ((keys + n - 1) / n + 63) / 64 * 64;
-    if (ch < 64) ch = 64;
+    int64_t ch = ((keys + n - 1) / n + 127) / 128 * 128;
+    if (ch < 128) ch = 128;
     *c = (int32_t)ch;
     *s = (int32_t)((keys + ch - 1) / ch);
   };
   split((int64_t)B * hkv * p.rbo, max_kv, kOwnBlocks, &p.so, &p.co);
-  p.cp = 64;
+  p.cp = 128;
   if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, kPrefixBlocks, &p.sp, &p.cp);
   if (p.sp == 0 && p.so <= 1) {
     p.so = 1;
@@ -252,7 +254,7 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   a.B = b->seqs;
   a.max_q = b->max_q;
   a.max_kv = b->max_kv;
-  a.pw = b->seq_pages;
+  a.pw = b->max_kv > 0 ? b->seq_pages : 0;
   a.q_start = b->q_start;
   a.kv_len = b->kv_len;
   a.pages = b->pages;

@@ -52,10 +52,10 @@ inline Div div_by(int32_t d) {
 // stay on the device).
 struct AttnPlan {
   bool rows;          // long queries: a block walks all keys of its 128 rows; else the keys are split
-  bool to, tp;        // split form: own keys / prefixes by Tiles (to: both), else by Keys
+  int32_t wo, wp;     // split form, own keys / prefixes: by Keys of 16 or 32 rows (1, 2), by Tiles (3); wo <= wp
   int32_t rbo, rbp;   // row blocks of a sequence / of a group
   int32_t so, sp;     // key splits of a sequence's own keys / of a prefix
-  int32_t co, cp;     // keys of a split (multiples of 64)
+  int32_t co, cp;     // keys of a split (multiples of 128)
   bool direct;        // one split in all: the outputs are written at once
   Div rbo_d, rbp_d, so_d, sp_d;
   size_t o_off, ws;   // split form: partial sums at o_off of the workspace, its size

@@ -343,6 +343,15 @@ def test_attention(name):
     Case(len(name), **ATT[name]).check()
 
 
+def test_attention_of_a_batch_without_keys():
+    """No key anywhere, a bound of none and a page table without columns: zeros."""
+    t = torch()
+    note("attention, no keys")
+    c = Case(1, nq=[2, 1], kv_len=[0, 0], groups=[0], prefix=[], hq=4, hkv=2, dim=128, page=16, kv="bf16")
+    c.batch = trs.AttnBatch(c.q_start, c.dlen, t.empty((2, 0), dtype=t.int32, device="cuda"), 2, 0)
+    assert (vals(c.run()) == 0).all()
+
+
 @pytest.mark.parametrize("name", ["drafted tokens", "prompts", "many rows on a prefix", "groups e4m3"])
 def test_attention_repeats_bit_for_bit(name):
     note("attention twice", name)
