@@ -90,7 +90,8 @@ struct Tiles {
     k1 = min(k1, bup);
     if (k0 >= k1) return;
     // Q is here before the first keys leave: a wait for it inside the loop
-    // would be one for them too (loads return in order; 8x2048 prompt: 187 us, 210 with it).
+    // would be one for them too (loads return in
+    // order; 8x2048 prompt: 187 us, 210 with it).
 #pragma unroll
     for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
     Stage g(st, pages, sh);
@@ -110,7 +111,7 @@ struct Tiles {
     g.store_v(sh.v[0]);
     wait_loads<0>();
     g.mend_v(sh.v[0], sh.odd[0], k0, blo, bup);
-    if (k0 + kTile < k1) g.load_k(st, k0 + kTile, k1, g.k_at(sh, 1));
+    if (F8 || k0 + kTile < k1) g.load_k(st, k0 + kTile, k1, g.k_at(sh, 1));
     wait_lds_barrier();
     f32x16 s;
     if (k0 < up) {
@@ -245,7 +246,10 @@ struct Tiles {
     }
   };
 
-  // The tile at k, in buffer B; `s` holds the scores of its first half.
+  // The tile at k, in buffer B; `s` holds the scores of its first half.  e4m3:
+  // the loads (to registers) do not depend on whether a tile follows, the last
+  // one is loaded again: else the compiler would count only the loads that
+  // leave on every path, and wait for younger ones too.
   template <int B>
   __device__ __forceinline__ void tile(Stage& g, const Stream& st, f32x16& s, int k, int k1, int lo, int up, int blo,
                                        int bup, float c, const int* ko, const int* vo, TilesLds<D>& sh) {
@@ -253,7 +257,7 @@ struct Tiles {
     const int mid = k + kTile / 2;
     constexpr int kHalf = kTile / 2 * D * 2;   // bytes of 32 keys
     float t;
-    if (__builtin_expect(more, 1)) g.load_v(st, g.v_at(sh, B ^ 1));
+    if (F8 || __builtin_expect(more, 1)) g.load_v(st, g.v_at(sh, B ^ 1));
     if (__builtin_expect(k < up, 1)) {
       step(s, t, sh.k[B] + kHalf, sh.v[B], c, ko, vo);
       unfinite(st, k, k, up, blo, sh.odd[B]);
@@ -263,8 +267,8 @@ struct Tiles {
       if constexpr (F8) g.store_k(sh.k[B ^ 1]);
       else wait_loads<KL>();   // the keys; the values are younger
       wait_lds_barrier();
-      if (__builtin_expect(k + 2 * kTile < k1, 1)) g.load_k(st, k + 2 * kTile, k1, g.k_at(sh, B));
     }
+    if (F8 || k + 2 * kTile < k1) g.load_k(st, k + 2 * kTile, k1, g.k_at(sh, B));
     if (__builtin_expect(mid < up, 1)) {
       step(s, t, sh.k[B ^ 1], sh.v[B] + kHalf, c, ko, vo);   // (the scores of a tile that is not there are not used)
       unfinite(st, mid, k, up, blo, sh.odd[B]);
