@@ -646,7 +646,8 @@ typedef struct dc_rope {
  * fp32, one rounding.  An e4m3 cache gets e4m3(x / scale), saturated at +-448
  * (infinities too; NaN stays NaN).
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
- * (a page's slots of one head span 1 GiB or more).  N = 0 is a no-op.
+ * (a page's slots of one head span 1 GiB or more, 2^24 tokens or more).
+ * N = 0 is a no-op.
  */
 dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_t* q, int64_t q_stride,
                        const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* pos,
@@ -704,7 +705,9 @@ typedef struct dc_attn_batch {
  * written for such sequences is unspecified.
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE (a page table too narrow for its
  * bound, q_heads no multiple of the kv heads), DC_ERR_ALIGN, DC_ERR_BUFFER,
- * DC_ERR_UNSUPPORTED (2^31 query rows or launched blocks).
+ * DC_ERR_UNSUPPORTED (2^24 launched blocks or more: those of one (sequence or
+ * group, kv head, 16 to 128 query rows, range of keys) each; for calls with
+ * partial sums 2^26 query rows or more).
  */
 size_t dc_attention_workspace_bytes(const dc_kv_cache* kv, const dc_attn_batch* b, int32_t q_heads, int32_t N);
 dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint16_t* q, int64_t q_stride,

@@ -27,6 +27,9 @@ bool rows_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb,
 
 bool mul_fits(int64_t a, int64_t b, int64_t lim) { return a == 0 || b <= lim / a; }
 
+// A launch's threads along x are numbered with 32 bits; blocks of 256.
+constexpr int64_t kMostBlocks = UINT32_MAX / 256;
+
 // The cache's shape and strides; fills the kernels' view of it.
 dc_status check_cache(const dc_kv_cache* c, dc::KvArgs* k) {
   if (!c) return DC_ERR_INVALID_ARG;
@@ -86,7 +89,7 @@ dc_status check_batch(const dc_kv_cache* kv, const dc_attn_batch* b, int32_t q_h
   return DC_OK;
 }
 
-// Blocks of either form, at most (64 bits: the launch needs 32).
+// Blocks of either form.
 int64_t blocks_of(const dc::AttnPlan& p, int64_t B, int64_t G, int64_t heads) {
   if (p.rows) return (B * heads + 7) / 8 * 8 * p.rbo;
   return B * heads * p.rbo * p.so + G * heads * p.rbp * p.sp;
@@ -177,6 +180,7 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
     return DC_ERR_INVALID_ARG;
   if (!slots) return DC_ERR_INVALID_ARG;
   if (!aligned(slots, 8)) return DC_ERR_ALIGN;
+  if (N > kMostBlocks) return DC_ERR_UNSUPPORTED;   // a block a token
   if (N == 0) return DC_OK;
   a.q = q;
   a.k = k;
@@ -232,7 +236,8 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   a.plan = dc::attn_plan(kv->heads, q_heads / kv->heads, kv->dim, N, b->seqs, b->max_q, b->max_kv, b->groups,
                          b->max_group_q, b->max_prefix);
   if (ws_bytes < a.plan.ws) return DC_ERR_BUFFER;
-  if (blocks_of(a.plan, b->seqs, b->groups, kv->heads) > INT32_MAX) return DC_ERR_UNSUPPORTED;
+  if (blocks_of(a.plan, b->seqs, b->groups, kv->heads) > kMostBlocks) return DC_ERR_UNSUPPORTED;
+  if (!a.plan.direct && ((int64_t)N * q_heads + 3) / 4 > kMostBlocks) return DC_ERR_UNSUPPORTED;   // the join
   if (N == 0 || b->seqs == 0 || b->max_q == 0) return DC_OK;   // no query: nothing to write
   a.q = q;
   a.y = y;

@@ -178,3 +178,15 @@ def test_binding_checks_types_and_shapes():
     with pytest.raises(ValueError):   # rows that are too short for the heads
         trs.dc_kv_append(c, None, torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16), None,
                          torch.zeros(4, dtype=torch.int64), None, None)
+
+
+def test_more_blocks_than_a_launch_takes(L):
+    """Refused before anything is launched (2^32 threads are one too many)."""
+    assert append(L, n=1 << 24, q=1 << 40, k=1 << 42, v=1 << 43, qo=1 << 44) == E.DC_ERR_UNSUPPORTED
+    few = dict(groups=0, group_start=None, prefix_len=None, prefix_pages=None)
+    # a block for every sequence and kv head
+    assert attend(L, b=batch(seqs=1 << 22, max_q=1, max_kv=16, **few), n=2, nws=1 << 60) == E.DC_ERR_UNSUPPORTED
+    # the rows whose partial sums are joined, four a block
+    b = batch(seqs=2, max_q=1, max_kv=100, max_group_q=1)
+    q, y = 1 << 40, 1 << 50
+    assert attend(L, b=b, q=q, y=y, n=1 << 23, nws=1 << 60) == E.DC_ERR_UNSUPPORTED
