@@ -66,10 +66,10 @@ dc_status check_cache(const dc_kv_cache* c, dc::KvArgs* k) {
   return DC_OK;
 }
 
-// A row-strided bf16 matrix [n][cols].
-dc_status check_rows(const void* p, int64_t stride, int64_t cols) {
+// A row-strided bf16 matrix [n][cols], within 2^47 bytes.
+dc_status check_rows(const void* p, int64_t stride, int64_t cols, int64_t n) {
   if (!p) return DC_ERR_INVALID_ARG;
-  if (stride < cols || stride > (INT64_C(1) << 40)) return DC_ERR_SHAPE;
+  if (stride < cols || !mul_fits(n > 1 ? n : 1, stride, INT64_C(1) << 46)) return DC_ERR_SHAPE;
   if (!aligned(p, 16) || stride % 8) return DC_ERR_ALIGN;
   return DC_OK;
 }
@@ -168,13 +168,13 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
     if (!aligned(rope->inv_freq, 8) || !aligned(pos, 4)) return DC_ERR_ALIGN;
   }
   if (q_heads > 0) {
-    if ((st = check_rows(q, q_stride, qc)) != DC_OK) return st;
-    if ((st = check_rows(q_out, q_out_stride, qc)) != DC_OK) return st;
+    if ((st = check_rows(q, q_stride, qc, N)) != DC_OK) return st;
+    if ((st = check_rows(q_out, q_out_stride, qc, N)) != DC_OK) return st;
     const bool in_place = q == q_out && q_stride == q_out_stride;
     if (!in_place && rows_meet(q, 2 * q_stride, 2 * qc, q_out, 2 * q_out_stride, 2 * qc, N)) return DC_ERR_INVALID_ARG;
   }
-  if ((st = check_rows(k, k_stride, kc)) != DC_OK) return st;
-  if ((st = check_rows(v, v_stride, kc)) != DC_OK) return st;
+  if ((st = check_rows(k, k_stride, kc, N)) != DC_OK) return st;
+  if ((st = check_rows(v, v_stride, kc, N)) != DC_OK) return st;
   if (q_heads > 0 && (rows_meet(k, 2 * k_stride, 2 * kc, q_out, 2 * q_out_stride, 2 * qc, N) ||
                       rows_meet(v, 2 * v_stride, 2 * kc, q_out, 2 * q_out_stride, 2 * qc, N)))
     return DC_ERR_INVALID_ARG;
@@ -220,8 +220,8 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   if ((st = check_batch(kv, b, q_heads, N)) != DC_OK) return st;
   if (!(scale > 0.f) || !std::isfinite(scale)) return DC_ERR_INVALID_ARG;
   const int64_t qc = (int64_t)q_heads * kv->dim;
-  if ((st = check_rows(q, q_stride, qc)) != DC_OK) return st;
-  if ((st = check_rows(y, y_stride, qc)) != DC_OK) return st;
+  if ((st = check_rows(q, q_stride, qc, N)) != DC_OK) return st;
+  if ((st = check_rows(y, y_stride, qc, N)) != DC_OK) return st;
   if (rows_meet(q, 2 * q_stride, 2 * qc, y, 2 * y_stride, 2 * qc, N)) return DC_ERR_INVALID_ARG;
   if (!ws) return DC_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return DC_ERR_ALIGN;

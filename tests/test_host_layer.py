@@ -190,3 +190,12 @@ def test_more_blocks_than_a_launch_takes(L):
     b = batch(seqs=2, max_q=1, max_kv=100, max_group_q=1)
     q, y = 1 << 40, 1 << 50
     assert attend(L, b=b, q=q, y=y, n=1 << 23, nws=1 << 60) == E.DC_ERR_UNSUPPORTED
+
+
+def test_strides_beyond_any_memory(L):
+    """Rows that would lie 2^48 bytes away: refused, and no product of 64 bits overflows on the way (the rows of q and
+    q_out then count as apart)."""
+    far = 1 << 40
+    assert append(L, n=1 << 23, qs=far, qos=far, q=1 << 40, qo=(1 << 40) + 4096, k=1 << 50, v=1 << 51) == E.DC_ERR_SHAPE
+    assert append(L, n=1 << 23, ks=far, q=1 << 40, qo=1 << 41, k=1 << 50, v=1 << 51) == E.DC_ERR_SHAPE
+    assert attend(L, n=1 << 23, qs=far, ys=far, q=1 << 40, y=(1 << 40) + 4096, nws=1 << 60) == E.DC_ERR_SHAPE
