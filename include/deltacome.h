@@ -692,7 +692,7 @@ typedef struct dc_attn_batch {
  *   q, y      device bf16 [N][q_heads * dim], rows q_stride / y_stride apart
  *             (multiples of 8 elements); must not overlap.  Rows behind the
  *             last sequence are left as they are
- *   scale     finite, > 0
+ *   scale     > 0, no subnormal, and finite times log2(e)
  *   ws        ws_bytes >= dc_attention_workspace_bytes(kv, b, q_heads, N)
  * A row that sees no key gets zeros.  What lies in slots that a row does not
  * see (infinities and NaN included) does not reach it.

@@ -1,6 +1,7 @@
 // Entry points of the decoder-layer operators (paged key/value cache, 4-bit
 // backbone): argument checks on the host, then one launcher.  No allocation,
 // no synchronization.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -218,7 +219,10 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   dc_status st = check_cache(kv, &a.kv);
   if (st != DC_OK) return st;
   if ((st = check_batch(kv, b, q_heads, N)) != DC_OK) return st;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return DC_ERR_INVALID_ARG;
+  // the kernels' exponentials are base 2; a factor of zero or infinity would
+  // turn masked or zero scores into NaN
+  const float base2 = (float)((double)scale * 1.4426950408889634074);
+  if (!(scale >= FLT_MIN) || !std::isfinite(base2)) return DC_ERR_INVALID_ARG;
   const int64_t qc = (int64_t)q_heads * kv->dim;
   if ((st = check_rows(q, q_stride, qc, N)) != DC_OK) return st;
   if ((st = check_rows(y, y_stride, qc, N)) != DC_OK) return st;
@@ -243,7 +247,7 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   a.y = y;
   a.qs = q_stride;
   a.ys = y_stride;
-  a.scale = (float)((double)scale * 1.4426950408889634074);   // the kernels' exponentials are base 2
+  a.scale = base2;
   a.hq = q_heads;
   a.gq = q_heads / kv->heads;
   a.hq_d = dc::div_by(a.hq);

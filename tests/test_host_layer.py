@@ -199,3 +199,12 @@ def test_strides_beyond_any_memory(L):
     assert append(L, n=1 << 23, qs=far, qos=far, q=1 << 40, qo=(1 << 40) + 4096, k=1 << 50, v=1 << 51) == E.DC_ERR_SHAPE
     assert append(L, n=1 << 23, ks=far, q=1 << 40, qo=1 << 41, k=1 << 50, v=1 << 51) == E.DC_ERR_SHAPE
     assert attend(L, n=1 << 23, qs=far, ys=far, q=1 << 40, y=(1 << 40) + 4096, nws=1 << 60) == E.DC_ERR_SHAPE
+
+
+@pytest.mark.parametrize("scale", [1e-45, 1e-38, 2.4e38, 3.4e38])
+def test_attention_scales_out_of_range(L, scale):
+    assert attend(L, n=2, scale=scale) == E.DC_ERR_INVALID_ARG
+
+
+def test_attention_scales_at_the_ends(L):
+    assert attend(L, scale=1.2e-38) == E.DC_OK and attend(L, scale=2.3e38) == E.DC_OK
