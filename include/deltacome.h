@@ -663,8 +663,8 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
  *             q_start[b] .. q_start[b+1]-1 of q (none is allowed)
  *   kv_len    [seqs]: keys in its own pages, its query tokens' among them (0
  *             is allowed)
- *   pages     [seqs][seq_pages]: page numbers; entries past the length are not
- *             read
+ *   pages     [seqs][seq_pages]: page numbers; entries past the length may be
+ *             anything
  *   group_start [groups+1] non-decreasing: sequences group_start[g] ..
  *             group_start[g+1]-1 share prefix g (none is allowed; sequences
  *             outside every group have no prefix)
@@ -691,9 +691,11 @@ typedef struct dc_attn_batch {
  * is read once for its group's rows.
  *   q, y      device bf16 [N][q_heads * dim], rows q_stride / y_stride apart
  *             (multiples of 8 elements); must not overlap.  Rows behind the
- *             last sequence are left as they are
+ *             last sequence, and in front of the first, are left as they are
  *   scale     > 0, no subnormal, and finite times log2(e)
- *   ws        ws_bytes >= dc_attention_workspace_bytes(kv, b, q_heads, N)
+ *   ws        ws_bytes >= dc_attention_workspace_bytes(kv, b, q_heads, N), 256-byte
+ *             aligned; holds nothing between calls, so calls that follow each
+ *             other may share one, and calls that may run at once may not
  * A row that sees no key gets zeros.  What lies in slots that a row does not
  * see (infinities and NaN included) does not reach it.
  * Arithmetic: bf16 products with fp32 sums; the weights enter the second

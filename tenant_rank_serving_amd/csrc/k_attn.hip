@@ -88,6 +88,7 @@ __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, con
         const float x[4] = {R.o[d][4 * i], R.o[d][4 * i + 1], R.o[d][4 * i + 2], R.o[d][4 * i + 3]};
         store_y<4>(reinterpret_cast<uint16_t*>(mine + i32 * kRow) + 32 * d + 8 * i + 4 * g, x, f);
       }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (other lanes wrote what a lane reads)
     constexpr int P = D / 8;   // pieces of a row
 #pragma unroll
     for (int i = 0; i < kTileRows * P / 64; ++i) {

@@ -631,3 +631,151 @@ def test_layer_step_of_many_tenants():
         g.replay()
         t.cuda.synchronize()
         assert np.array_equal(host_bits(out), first)
+
+
+# ------------------------------------------------- further calls of each
+def test_append_every_bit_pattern():
+    """Without a rotation every bf16 number, subnormal ones and infinities included, passes as it is (NaN as some NaN)."""
+    t = torch()
+    note("append, every bit pattern")
+    n, dim = 512, 128
+    pool = Pool("bf16", n // 16, 1, 16, dim, np.random.default_rng(0))
+    cache = pool.upload()
+    every = np.arange(1 << 16, dtype=np.uint16)
+    x = t.from_numpy(every.view(np.int16).reshape(n, dim)).cuda().view(t.bfloat16)
+    out = t.zeros_like(x)
+    trs.dc_kv_append(cache, x, x, x, None, t.arange(n, dtype=t.int64, device="cuda"), None, out)
+    t.cuda.synchronize()
+    nan = np.isnan(vals(every))
+    for got in [host_bits(out)] + pool.download():
+        got = got.reshape(-1)
+        assert np.array_equal(got[~nan], every[~nan]) and np.isnan(vals(got[nan])).all()
+
+
+def test_append_captured_on_another_stream():
+    """Replays follow the positions and slots that changed since; every other slot stays."""
+    t = torch()
+    note("append, captured")
+    rng = np.random.default_rng(6)
+    n, hq, hkv, dim, pages = 5, 4, 2, 64, 3
+    rope = trs.Rope(t.rand(dim // 2, dtype=t.float64, device="cuda"))
+    q, k, v = (dev_bf16(rng.normal(size=(n, h * dim))) for h in (hq, hkv, hkv))
+    pos, slots = t.zeros(n, dtype=t.int32, device="cuda"), t.zeros(n, dtype=t.int64, device="cuda")
+    pools = [Pool("bf16", pages, hkv, 16, dim, rng) for _ in range(2)]
+    caches = [p.upload() for p in pools]
+    outs = [t.zeros_like(q) for _ in range(2)]
+    side = t.cuda.Stream()
+    g = t.cuda.CUDAGraph()
+    slots.copy_(t.arange(n))
+    t.cuda.synchronize()
+    with t.cuda.graph(g, stream=side):
+        trs.dc_kv_append(caches[0], q, k, v, pos, slots, rope, outs[0])
+    for step in range(4):
+        pos.copy_(dev_i32(rng.integers(0, 5000, n)))
+        slots.copy_(t.from_numpy(rng.permutation(pages * 16)[:n].astype(np.int64)))
+        t.cuda.synchronize()
+        with t.cuda.stream(side):
+            g.replay()
+        trs.dc_kv_append(caches[1], q, k, v, pos, slots, rope, outs[1])
+        t.cuda.synchronize()
+        assert np.array_equal(host_bits(outs[0]), host_bits(outs[1])), step
+        for a, b in zip(*(p.download() for p in pools)):
+            assert np.array_equal(a, b), step
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("nq", [[1, 1], [1] * 6, [1] * 12, [5, 3], [5, 8], [9, 1, 14]])
+def test_attention_rows_of_every_number(nq, dim, kv):
+    """4 query heads a kv head: up to 16, up to 32 and more rows of own keys and of a prefix."""
+    note("attention, rows", nq, dim, kv)
+    own = [200 + 37 * i for i in range(len(nq))]
+    Case(len(nq) + dim, nq=nq, kv_len=own, groups=[0, len(nq)], prefix=[301], hq=8, hkv=2, dim=dim, page=16, kv=kv).check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", [2, 5])
+def test_attention_of_few_rows_does_not_see_later_tokens(heads, dim, kv):
+    """12 and 30 rows of a kv head: infinities and NaN of a later token reach it and those behind it only."""
+    note("attention, later tokens, few rows", heads, dim, kv)
+    c = Case(heads, nq=[6, 3], kv_len=[150, 40], groups=[0], prefix=[], hq=2 * heads, hkv=2, dim=dim, page=16, kv=kv)
+    clean = c.run().copy()
+    i = 150 - 6 + 4                              # the key of query token 4
+    p, s = c.tables[0][i // c.page], i % c.page
+    nan, inf = (0x7FC0, 0x7F80) if kv == "bf16" else (0x7F, 0xFF)
+    c.pool.v[p, :, s, ::2] = nan
+    c.pool.v[p, :, s, 1::2] = inf
+    c.reload()
+    got = c.run()
+    assert np.array_equal(got[:4], clean[:4]) and np.array_equal(got[6:], clean[6:])
+    assert not np.isfinite(vals(got[4:6])).any()
+
+
+@pytest.mark.parametrize("name", ["odd lengths", "one key", "groups e4m3", "drafted tokens, more rows", "prompts",
+                                  "prompts, shared heads"])
+def test_attention_rows_in_front_of_the_first_sequence(name):
+    """They stay as they are, like those behind the last; the sequences' results do not depend on where they lie."""
+    t = torch()
+    note("attention, rows in front", name)
+    c = Case(21, **ATT[name])
+    want = c.run().copy()
+    c.q_start.add_(2)
+    c.dq[2:c.n + 2] = c.dq[:c.n].clone()
+    c.dq[:2] = float("nan")
+    c.dy.fill_(-5.0)
+    trs.dc_attention(c.cache, c.dq, c.batch, c.scale, c.dy, c.ws)
+    t.cuda.synchronize()
+    got = host_bits(c.dy).reshape(-1, c.hq, c.dim)
+    assert (vals(got[:2]) == -5.0).all() and (vals(got[c.n + 2:]) == -5.0).all()
+    assert np.array_equal(got[2:c.n + 2], want)
+
+
+def test_attention_two_graphs_on_one_workspace():
+    """Nothing is kept in a workspace: two captured calls that use the same one, replayed in turn."""
+    t = torch()
+    note("attention, one workspace")
+    cs = [Case(30 + i, **ATT[n]) for i, n in enumerate(["groups e4m3", "many rows on a prefix"])]
+    want = [c.run().copy() for c in cs]
+    ws = max((c.ws for c in cs), key=lambda w: w.numel())
+    graphs = []
+    for c in cs:
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            trs.dc_attention(c.cache, c.dq, c.batch, c.scale, c.dy, ws)
+        graphs.append(g)
+    for step in range(3):
+        for c in cs:
+            c.dy.fill_(-5.0)
+        for g in graphs[::1 if step % 2 else -1]:
+            g.replay()
+        t.cuda.synchronize()
+        for c, w in zip(cs, want):
+            assert np.array_equal(host_bits(c.dy).reshape(-1, c.hq, c.dim)[:c.n], w), step
+
+
+@pytest.mark.parametrize("t_", [1, 40])
+def test_w4_captured_and_what_is_not_finite(t_):
+    """Replays follow x; a token that is not finite spoils its own row only; nothing behind y's rows is written."""
+    t = torch()
+    note("w4 captured", t_)
+    rng = np.random.default_rng(40 + t_)
+    out, inn = 384, 640
+    view = w4_case(rng, out, inn)[3]
+    x = dev_bf16(rng.normal(size=(t_ + 1, inn)))
+    y = t.full((t_ + 2, out), -5.0, dtype=t.bfloat16, device="cuda")
+    want = t.empty((t_, out), dtype=t.bfloat16, device="cuda")
+    g = t.cuda.CUDAGraph()
+    t.cuda.synchronize()
+    with t.cuda.graph(g):
+        trs.dc_apply_w4(view, x[:t_], y[:t_])
+    for step in range(3):
+        x.copy_(x.roll(1, 0))
+        g.replay()
+        trs.dc_apply_w4(view, x[:t_], want)
+        t.cuda.synchronize()
+        assert np.array_equal(host_bits(y[:t_]), host_bits(want)) and (y[t_:] == -5).all(), step
+    x[0, 77] = float("inf")
+    g.replay()
+    t.cuda.synchronize()
+    assert not t.isfinite(y[0]).any() and np.array_equal(host_bits(y[1:t_]), host_bits(want[1:]))
