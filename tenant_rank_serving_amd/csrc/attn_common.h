@@ -95,16 +95,17 @@ struct Pages {
   int base, pg;
   __device__ __forceinline__ void fill(const Stream& st, int p) {
     base = p;
-    pg = 0;
-    if (st.width == 0) return;   // a call without keys may come without a table
-    pg = st.table[min(p + (int)(threadIdx.x & 63), st.width - 1)];
-    pg = (unsigned)pg < (unsigned)st.num_pages ? pg : 0;   // never outside the cache
+    pg = st.table[min(p + (int)(threadIdx.x & 63), st.width - 1)];   // (used, and so waited for, by offset)
   }
   // Byte offset of key `at` (the first of 16 that share a page); ascending.
   __device__ __forceinline__ int64_t offset(const Stream& st, int at) {
     const int p = at >> st.shift;
-    if (__builtin_expect(p - base >= 64, 0)) fill(st, p);
-    const int64_t page = __builtin_amdgcn_readlane(pg, p - base);
+    if (__builtin_expect(p - base >= 64, 0)) {
+      fill(st, p);
+      asm volatile("" : "+v"(pg));   // waited for here, not by the code that both ways share
+    }
+    const int n = __builtin_amdgcn_readlane(pg, p - base);
+    const int64_t page = (unsigned)n < (unsigned)st.num_pages ? n : 0;   // never outside the cache
     return page * st.page_stride + (int64_t)(at & ((1 << st.shift) - 1)) * st.slot_stride;
   }
 };

@@ -89,11 +89,6 @@ struct Tiles {
                                        int bup, float c, bool live, TilesLds<D>& sh) {
     k1 = min(k1, bup);
     if (k0 >= k1) return;
-    // Q is here before the first keys leave: a wait for it inside the loop
-    // would be one for them too (loads return in
-    // order; 8x2048 prompt: 187 us, 210 with it).
-#pragma unroll
-    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
     Stage g(st, pages, sh);
     const int lane = threadIdx.x & 63, half = lane >> 5, i32 = lane & 31;
     int ko[KS], vo[DT];
@@ -110,6 +105,10 @@ struct Tiles {
     g.store_k(sh.k[0]);
     g.store_v(sh.v[0]);
     wait_loads<0>();
+    // Q is here too: a wait for it inside the loop would be one for younger
+    // loads (they return in order; 8x2048 prompt: 187 us, 210 with it)
+#pragma unroll
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
     g.mend_v(sh.v[0], sh.odd[0], k0, blo, bup);
     if (F8 || k0 + kTile < k1) g.load_k(st, k0 + kTile, k1, g.k_at(sh, 1));
     wait_lds_barrier();

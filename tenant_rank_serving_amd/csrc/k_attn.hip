@@ -274,6 +274,10 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_rows(AttnArgs a) {
   const int pair = p8 * 8 + xcd;
   if (pair >= a.B * a.kv.heads) return;
   const int b = a.hkv_d.of(pair), h = pair - b * a.kv.heads;
+  // the page numbers are on their way while the lengths are read
+  const Stream st = own_stream(a, h, b);
+  Pages pages;
+  pages.fill(st, 0);
   const Item own = own_item(a, b);
   const int blk0 = rblk * kBlockRows;
   if (blk0 >= own.rows) return;
@@ -283,18 +287,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_rows(AttnArgs a) {
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, own, row0, h, flip);
-  Pages pages;
   if constexpr (PRE) {   // the group's prefix, all of it
     const int gr = group_of(a, b);
     Item it = own;
     it.len = gr < 0 ? 0 : clampi(a.p_len[gr], 0, a.max_pre);
     it.causal = false;
-    const Stream st = prefix_stream(a, h, max(gr, 0));
-    pages.fill(st, 0);
-    tiles_walk<D, F8>(a, it, st, pages, R, blk0, h, 0, it.len, c, sh);
+    const Stream ps = prefix_stream(a, h, max(gr, 0));
+    Pages pp;
+    pp.fill(ps, 0);
+    tiles_walk<D, F8>(a, it, ps, pp, R, blk0, h, 0, it.len, c, sh);
   }
-  const Stream st = own_stream(a, h, b);
-  pages.fill(st, 0);
   tiles_walk<D, F8>(a, own, st, pages, R, blk0, h, 0, own.len, c, sh);
   put_tiles<D, F8>(a, own, R, row0, h, 0, vs, sh);
 }

@@ -263,10 +263,10 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   a.B = b->seqs;
   a.max_q = b->max_q;
   a.max_kv = b->max_kv;
-  a.pw = b->max_kv > 0 ? b->seq_pages : 0;
+  a.pw = b->max_kv > 0 ? b->seq_pages : 1;
   a.q_start = b->q_start;
   a.kv_len = b->kv_len;
-  a.pages = b->pages;
+  a.pages = b->max_kv > 0 ? b->pages : b->kv_len;   // (the kernels read an entry ahead; without keys none is used)
   const bool pre = b->groups > 0 && b->max_prefix > 0 && b->max_group_q > 0;
   a.G = pre ? b->groups : 0;
   a.max_gq = b->max_group_q;
