@@ -1,6 +1,5 @@
 // The walk for more than 32 query rows: a block takes 128 rows, wave w rows
-// 32w .. 32w+31, and its keys come through LDS in tiles of 64 that all waves
-// share.  Included inside namespace dc, anonymous namespace, of k_attn.hip,
+// 32w .. 32w+31, and its keys come through LDS in tiles that all waves share.  Included inside namespace dc, anonymous namespace, of k_attn.hip,
 // behind attn_common.h.
 //
 // Products transposed as for few rows, S^T = K Q^T and O^T = V^T P^T, here
@@ -12,7 +11,7 @@
 //   V^T operand A: element 32 d + l%32, the same 8 keys: two transposing reads
 //       of LDS (ds_read_b64_tr_b16: of 16 lanes, lane 4r + c supplies elements
 //       4c .. 4c+3 of row r, lane j receives element j of the 4 rows).
-//   LDS holds K and V as the cache does, [64 keys][D] in bf16, the 16-byte
+//   LDS holds K and V as the cache does, [keys][D] in bf16, the 16-byte
 //       pieces of a key permuted by an XOR with its number such that the lanes
 //       that are served together reach different banks (key_swizzle,
 //       value_swizzle).  bf16 keys go straight to LDS (global_load_lds, no
@@ -24,7 +23,7 @@ __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-constexpr int kTile = 64;        // keys of a tile
+constexpr int kStepKeys = 32;        // keys of a step
 constexpr int kTileRows = 32;    // rows of a wave
 constexpr int kBlockRows = kWaves * kTileRows;
 
@@ -36,15 +35,18 @@ template <int D> __device__ __forceinline__ int value_swizzle(int key) {
   return D == 128 ? (key & 3) << 2 : ((key >> 1) & 1) << 2;
 }
 
-template <int D>
+// bf16: three tiles of one step; e4m3: two of two steps.
+template <int D, bool F8>
 struct TilesLds {
-  alignas(256) uint8_t k[2][kTile * D * 2];
-  alignas(256) uint8_t v[2][kTile * D * 2];
-  uint32_t odd[2][kWaves];       // of a tile with masks: some of the values that a wave carried are not finite
+  static constexpr int kTiles = F8 ? 2 : 3, kKeys = F8 ? 2 * kStepKeys : kStepKeys;
+  alignas(256) uint8_t k[kTiles][kKeys * D * 2];
+  alignas(256) uint8_t v[kTiles][kKeys * D * 2];
+  uint32_t odd[kTiles][kWaves];       // of a tile with masks: some of the values that a wave carried are not finite
 };
 
 template <int D, bool F8>
 struct Tiles {
+  typedef TilesLds<D, F8> Lds;
   static constexpr int KS = D / 16;   // products of 32 keys' scores
   static constexpr int DT = D / 32;   // 32-element tiles of the result
   uint4 q[KS];
@@ -78,18 +80,14 @@ struct Tiles {
   // wave's rows all see the keys below lo and none see those from up on; blo,
   // bup: the block's.
   //
-  // Half tiles of 32 keys: step h multiplies the keys of half h + 1, takes the
-  // exponentials of half h and multiplies its values, in one stretch of code
-  // without branches, so that the matrix core and the vector unit work at the
-  // same time within a wave.  What a maximum moves is decided between steps.
-  // K of the next tile is needed in a tile's second step and V in the next
-  // tile's first; each is on its way for two steps.  With two buffers, one
-  // barrier a step.
+  // Step h multiplies the keys of step h + 1, takes the exponentials of step h
+  // and multiplies its values, in one stretch of code without branches, so
+  // that the matrix core and the vector unit work at the same time within a
+  // wave.  What a maximum moves is decided between steps.
   __device__ __forceinline__ void walk(const Stream& st, const Pages& pages, int k0, int k1, int lo, int up, int blo,
-                                       int bup, float c, bool live, TilesLds<D>& sh) {
+                                       int bup, float c, bool live, Lds& sh) {
     k1 = min(k1, bup);
     if (k0 >= k1) return;
-    Stage g(st, pages, sh);
     const int lane = threadIdx.x & 63, half = lane >> 5, i32 = lane & 31;
     int ko[KS], vo[DT];
 #pragma unroll
@@ -100,17 +98,25 @@ struct Tiles {
       vo[d] = (4 * half + r) * (D * 2) +
               (((4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ value_swizzle<D>(r)) * 16) + (lane & 1) * 8;
     if (!live) up = k0;   // no key is of interest
-    g.load_k(st, k0, k1, g.k_at(sh, 0));
-    g.load_v(st, g.v_at(sh, 0));
-    g.store_k(sh.k[0]);
-    g.store_v(sh.v[0]);
-    wait_loads<0>();
-    // Q is here too: a wait for it inside the loop would be one for younger
-    // loads (they return in order; 8x2048 prompt: 187 us, 210 with it)
-#pragma unroll
-    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
-    g.mend_v(sh.v[0], sh.odd[0], k0, blo, bup);
-    if (F8 || k0 + kTile < k1) g.load_k(st, k0 + kTile, k1, g.k_at(sh, 1));
+    Stage g(st, pages, sh);
+    if constexpr (F8) {
+      g.load_k(st, k0, k1);
+      g.load_v(st);
+      g.store_k(sh.k[0]);
+      g.store_v(sh.v[0]);
+      arrived();
+      mend_v(sh.v[0], sh.odd[0], k0, blo, bup);
+      g.load_k(st, k0 + kTile, k1);
+    } else {
+      g.load_k(st, k0, k1, 0);
+      g.load_v(st, 0);
+      if (k0 + kTile < k1) g.load_k(st, k0 + kTile, k1, 1);
+      wait_loads<0>();
+      arrived();
+      if (k0 + kTile < k1) g.load_v(st, 1);
+      if (k0 + 2 * kTile < k1) g.load_k(st, k0 + 2 * kTile, k1, 2);
+      mend_v(sh.v[0], sh.odd[0], k0, blo, bup);
+    }
     wait_lds_barrier();
     f32x16 s;
     if (k0 < up) {
@@ -120,18 +126,28 @@ struct Tiles {
       for (int i = 0; i < KS; ++i) s = mfma32(*reinterpret_cast<const uint4*>(sh.k[0] + ko[i]), q[i], s);
       prepare(s, largest(s), k0, lo, c);
     }
-    for (int k = k0; k < k1; k += 2 * kTile) {
-      tile<0>(g, st, s, k, k1, lo, up, blo, bup, c, ko, vo, sh);
-      if (k + kTile < k1) tile<1>(g, st, s, k + kTile, k1, lo, up, blo, bup, c, ko, vo, sh);
+    if constexpr (F8) {
+      for (int k = k0; k < k1; k += 2 * kTile) {
+        two_steps<0>(g, st, s, k, k1, lo, up, blo, bup, c, ko, vo, sh);
+        if (k + kTile < k1) two_steps<1>(g, st, s, k + kTile, k1, lo, up, blo, bup, c, ko, vo, sh);
+      }
+    } else {
+      wait_lds_barrier();   // the first keys' place is free
+      for (int k = k0; k < k1; k += 3 * kTile) {
+        one_step<0>(g, st, s, k, k1, lo, up, blo, bup, c, ko, vo, sh);
+        if (k + kTile < k1) one_step<1>(g, st, s, k + kTile, k1, lo, up, blo, bup, c, ko, vo, sh);
+        if (k + 2 * kTile < k1) one_step<2>(g, st, s, k + 2 * kTile, k1, lo, up, blo, bup, c, ko, vo, sh);
+      }
     }
     wait_lds_barrier();   // the buffers are free
   }
 
  private:
-  static constexpr int KB = F8 ? 1 : 2;              // bytes of an element of the cache
-  static constexpr int KL = 16 * D * KB / 1024;      // 16-byte pieces of a wave's 16 keys, a lane
-  static constexpr int KP = D * KB / 16;             // pieces of a key
-  static constexpr int KI = 64 / KP;                 // keys of a wave's load
+  static constexpr int kTile = Lds::kKeys;
+  static constexpr int KW = kTile / kWaves;                       // keys of a tile that a wave carries (one page)
+  static constexpr int KL = KW * D * (F8 ? 1 : 2) / 1024;         // 16-byte loads of theirs, a lane
+  static constexpr int KP = D * (F8 ? 1 : 2) / 16;                // 16-byte pieces of a key
+  static constexpr int KI = 64 / KP;                              // keys of a wave's load
 
   // At most N loads of the wave still on their way.
   template <int N> static __device__ __forceinline__ void wait_loads() {
@@ -141,58 +157,70 @@ struct Tiles {
   static __device__ __forceinline__ void wait_lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
+  // Q is here: a wait for it inside the loop would be one for younger loads
+  // (they return in order; 8x2048 prompt: 187 us, 210 with it).
+  __device__ __forceinline__ void arrived() {
+#pragma unroll
+    for (int i = 0; i < KS; ++i) asm volatile("" : "+v"(q[i].x), "+v"(q[i].y), "+v"(q[i].z), "+v"(q[i].w));
+  }
 
-  // A wave's part of a tile on its way from the cache to LDS: wave w carries
-  // keys 16w .. 16w+15 (one page).
-  struct Stage {
-    Words<4> kr[F8 ? KL : 1], vr[F8 ? KL : 1];   // e4m3: codes to be converted
+  // A wave's part of the tiles on their way from the cache to LDS: wave w
+  // carries keys KW w .. of each.  bf16: straight to LDS.
+  struct Direct {
     Pages pages;
     int64_t off;
-    int wave, ko[F8 ? 1 : KL], vo;   // the lane's offsets in 16 keys' rows
-    __device__ __forceinline__ Stage(const Stream& st, const Pages& p, const TilesLds<D>& sh) : pages(p) {
+    int wave, ko[KL], vo;   // the lane's offsets in the keys' rows
+    uint32_t at;            // LDS address of the wave's part of the first tile of keys
+    __device__ __forceinline__ Direct(const Stream& st, const Pages& p, const Lds& sh) : pages(p) {
       const int lane = threadIdx.x & 63;
       wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-      base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)&sh.k[0][0] + wave * (16 * D * 2);
+      at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)&sh.k[0][0] + wave * (KW * D * 2);
       const int key = lane / KP, pos = lane % KP;   // LDS takes 16 bytes a lane, in the order of the lanes
-      if constexpr (F8) {
-        ko[0] = vo = key * st.slot_stride + pos * 16;
-      } else {
 #pragma unroll
-        for (int i = 0; i < KL; ++i) ko[i] = key * st.slot_stride + (pos ^ key_swizzle<D>(key + KI * i)) * 16;
-        vo = key * st.slot_stride + (pos ^ value_swizzle<D>(key)) * 16;
-      }
-    }
-    // LDS addresses of the wave's part of buffer b
-    uint32_t base;
-    __device__ __forceinline__ uint32_t k_at(const TilesLds<D>& sh, int b) const { return base + b * (kTile * D * 2); }
-    __device__ __forceinline__ uint32_t v_at(const TilesLds<D>& sh, int b) const {
-      return base + (uint32_t)sizeof(sh.k) + b * (kTile * D * 2);
+      for (int i = 0; i < KL; ++i)
+        ko[i] = key * st.slot_stride + (pos ^ key_swizzle<D>(KW * wave + key + KI * i)) * 16;
+      vo = key * st.slot_stride + (pos ^ value_swizzle<D>(key)) * 16;
     }
     // 16 bytes a lane from base + voff to lds + 16 lane
-    static __device__ __forceinline__ void to_lds(const uint8_t* base, int voff, uint32_t at) {
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(voff), "s"(base) : "memory");
+    static __device__ __forceinline__ void to_lds(const uint8_t* base, int voff, uint32_t lds) {
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
     }
-    // the keys of the tile at k, and where its values are; at: where in LDS
-    // the wave's part begins
-    __device__ __forceinline__ void load_k(const Stream& st, int k, int k1, uint32_t at) {
-      off = pages.offset(st, min(k + 16 * wave, (k1 - 1) & ~15));
+    // the keys of the tile at k into buffer b, and where its values are
+    __device__ __forceinline__ void load_k(const Stream& st, int k, int k1, int b) {
+      off = pages.offset(st, min(k + KW * wave, (k1 - 1) & -KW));
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const uint8_t* p = st.k + off + (int64_t)(KI * i) * st.slot_stride;
-        if constexpr (F8) kr[i] = load_words<4>(p + ko[0]);
-        else to_lds(p, ko[i], at + i * 1024);
-      }
+      for (int i = 0; i < KL; ++i)
+        to_lds(st.k + off + (int64_t)(KI * i) * st.slot_stride, ko[i], at + b * (kTile * D * 2) + i * 1024);
     }
     // the values of the tile whose keys were loaded last
-    __device__ __forceinline__ void load_v(const Stream& st, uint32_t at) {
+    __device__ __forceinline__ void load_v(const Stream& st, int b) {
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const uint8_t* p = st.v + off + (int64_t)(KI * i) * st.slot_stride;
-        if constexpr (F8) vr[i] = load_words<4>(p + vo);
-        else to_lds(p, vo, at + i * 1024);
-      }
+      for (int i = 0; i < KL; ++i)
+        to_lds(st.v + off + (int64_t)(KI * i) * st.slot_stride, vo,
+               at + (uint32_t)sizeof(Lds::k) + b * (kTile * D * 2) + i * 1024);
     }
-    // e4m3: the codes that were loaded, converted
+  };
+
+  // e4m3: codes to registers, to be converted on their way to LDS.
+  struct Codes {
+    Words<4> kr[KL], vr[KL];
+    Pages pages;
+    int64_t off;
+    int wave, ko;   // the lane's offset in the keys' rows
+    __device__ __forceinline__ Codes(const Stream& st, const Pages& p, const Lds&) : pages(p) {
+      const int lane = threadIdx.x & 63;
+      wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      ko = lane / KP * st.slot_stride + lane % KP * 16;
+    }
+    __device__ __forceinline__ void load_k(const Stream& st, int k, int k1) {
+      off = pages.offset(st, min(k + KW * wave, (k1 - 1) & -KW));
+#pragma unroll
+      for (int i = 0; i < KL; ++i) kr[i] = load_words<4>(st.k + off + (int64_t)(KI * i) * st.slot_stride + ko);
+    }
+    __device__ __forceinline__ void load_v(const Stream& st) {
+#pragma unroll
+      for (int i = 0; i < KL; ++i) vr[i] = load_words<4>(st.v + off + (int64_t)(KI * i) * st.slot_stride + ko);
+    }
     static __device__ __forceinline__ void store(const Words<4>& w, uint8_t* row, int cc, int swizzle) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -200,84 +228,108 @@ struct Tiles {
             uint4{cvt2(w.w[2 * u], false), cvt2(w.w[2 * u], true), cvt2(w.w[2 * u + 1], false), cvt2(w.w[2 * u + 1], true)};
     }
     __device__ __forceinline__ void store_k(uint8_t* lds) {
-      if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < KL; ++i) {
-          const int lane = threadIdx.x & 63, key = lane / KP + KI * i;
-          store(kr[i], lds + (16 * wave + key) * (D * 2), lane % KP, key_swizzle<D>(key));
-        }
+      for (int i = 0; i < KL; ++i) {
+        const int lane = threadIdx.x & 63, key = KW * wave + lane / KP + KI * i;
+        store(kr[i], lds + key * (D * 2), lane % KP, key_swizzle<D>(key));
       }
     }
     __device__ __forceinline__ void store_v(uint8_t* lds) {
-      if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < KL; ++i) {
-          const int lane = threadIdx.x & 63, key = lane / KP + KI * i;
-          store(vr[i], lds + (16 * wave + key) * (D * 2), lane % KP, value_swizzle<D>(key));
-        }
+      for (int i = 0; i < KL; ++i) {
+        const int lane = threadIdx.x & 63, key = KW * wave + lane / KP + KI * i;
+        store(vr[i], lds + key * (D * 2), lane % KP, value_swizzle<D>(key));
       }
-    }
-    // The tile at k, if it has masks: values that no row of the block sees
-    // count as zero (the slots may hold anything), and so do, for now, those
-    // that are not finite.  The wave's own 16 keys, once they are in LDS.
-    __device__ __forceinline__ void mend_v(uint8_t* lds, uint32_t* odd, int k, int blo, int bup) {
-      if (__builtin_expect(k + kTile <= blo, 1)) return;
-      const int lane = threadIdx.x & 63;
-      if constexpr (F8) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (one wave wrote, other lanes read)
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint4* p = reinterpret_cast<uint4*>(lds + (wave * (D / 32) + i) * 1024 + lane * 16);
-        const bool dead = k + 16 * wave + (i * 64 + lane) / (D / 8) >= bup;
-        const uint4 u = *p;
-        uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = dead ? 0u : w[j];
-          const uint32_t bad = not_finite<false>(w[j]);
-          w[j] = only_finite<false>(w[j], bad);
-          any |= bad;
-        }
-        *p = uint4{w[0], w[1], w[2], w[3]};
-      }
-      const bool found = __builtin_amdgcn_ballot_w64(any != 0) != 0;
-      if (lane == 0) odd[wave] = found;
     }
   };
+  typedef std::conditional_t<F8, Codes, Direct> Stage;
 
-  // The tile at k, in buffer B; `s` holds the scores of its first half.  e4m3:
-  // the loads (to registers) do not depend on whether a tile follows, the last
-  // one is loaded again: else the compiler would count only the loads that
-  // leave on every path, and wait for younger ones too.
+  // The values of the tile at k, if it has masks: those that no row of the
+  // block sees count as zero (the slots may hold anything), and so do, for
+  // now, those that are not finite.  The wave's own keys, once they are in LDS.
+  static __device__ __forceinline__ void mend_v(uint8_t* lds, uint32_t* odd, int k, int blo, int bup) {
+    if (__builtin_expect(k + kTile <= blo, 1)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (F8) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (one wave wrote, other lanes read)
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < KW * D * 2 / 1024; ++i) {
+      uint4* p = reinterpret_cast<uint4*>(lds + wave * (KW * D * 2) + i * 1024 + lane * 16);
+      const bool dead = k + KW * wave + (i * 64 + lane) / (D / 8) >= bup;
+      const uint4 u = *p;
+      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = dead ? 0u : w[j];
+        const uint32_t bad = not_finite<false>(w[j]);
+        w[j] = only_finite<false>(w[j], bad);
+        any |= bad;
+      }
+      *p = uint4{w[0], w[1], w[2], w[3]};
+    }
+    const bool found = __builtin_amdgcn_ballot_w64(any != 0) != 0;
+    if (lane == 0) odd[wave] = found;
+  }
+
+  // bf16: the step at k, its values in buffer B and the next step's keys in
+  // B + 1; `s` holds its scores.  The values of the step after the next and
+  // the keys of the one behind that set out, into the places that the step
+  // before freed: each is on its way for two steps, with one barrier a step.
+  // Three tiles of 32 keys take 48 KB (D = 128), so three blocks share a CU
+  // (three waves a SIMD at 160 registers).
   template <int B>
-  __device__ __forceinline__ void tile(Stage& g, const Stream& st, f32x16& s, int k, int k1, int lo, int up, int blo,
-                                       int bup, float c, const int* ko, const int* vo, TilesLds<D>& sh) {
+  __device__ __forceinline__ void one_step(Stage& g, const Stream& st, f32x16& s, int k, int k1, int lo, int up, int blo,
+                                           int bup, float c, const int* ko, const int* vo, Lds& sh) {
+    constexpr int N = (B + 1) % 3, P = (B + 2) % 3;
     const bool more = k + kTile < k1;
-    const int mid = k + kTile / 2;
-    constexpr int kHalf = kTile / 2 * D * 2;   // bytes of 32 keys
+    if (k + 2 * kTile < k1) g.load_v(st, P);
+    if (k + 3 * kTile < k1) g.load_k(st, k + 3 * kTile, k1, B);
     float t;
-    if (F8 || __builtin_expect(more, 1)) g.load_v(st, g.v_at(sh, B ^ 1));
     if (__builtin_expect(k < up, 1)) {
-      step(s, t, sh.k[B] + kHalf, sh.v[B], c, ko, vo);
-      unfinite(st, k, k, up, blo, sh.odd[B]);
-      if (__builtin_expect(mid < up, 1)) prepare(s, t, mid, lo, c);
-    }
-    if (__builtin_expect(more, 1)) {
-      if constexpr (F8) g.store_k(sh.k[B ^ 1]);
-      else wait_loads<KL>();   // the keys; the values are younger
-      wait_lds_barrier();
-    }
-    if (F8 || k + 2 * kTile < k1) g.load_k(st, k + 2 * kTile, k1, g.k_at(sh, B));
-    if (__builtin_expect(mid < up, 1)) {
-      step(s, t, sh.k[B ^ 1], sh.v[B] + kHalf, c, ko, vo);   // (the scores of a tile that is not there are not used)
-      unfinite(st, mid, k, up, blo, sh.odd[B]);
+      step(s, t, sh.k[N], sh.v[B], c, ko, vo);   // (the scores of a step that is not there are not used)
+      unfinite(st, k, k + kTile, up, blo, sh.odd[B]);
       if (__builtin_expect(more && k + kTile < up, 1)) prepare(s, t, k + kTile, lo, c);
     }
     if (__builtin_expect(more, 1)) {
-      if constexpr (F8) g.store_v(sh.v[B ^ 1]);
-      else if (k + 2 * kTile < k1) wait_loads<KL>();   // the values; the next keys are younger
+      if (k + 3 * kTile < k1) wait_loads<2 * KL>();   // the next step's values and the keys behind; younger: this step's
       else wait_loads<0>();
-      g.mend_v(sh.v[B ^ 1], sh.odd[B ^ 1], k + kTile, blo, bup);
+      mend_v(sh.v[N], sh.odd[N], k + kTile, blo, bup);
+      wait_lds_barrier();
+    }
+  }
+
+  // e4m3: the two steps of the tile at k, in buffer B; `s` holds the scores of
+  // the first.  K of the next tile is needed in the second step and V in the
+  // next tile's first; each is on its way for two steps.  The loads (to
+  // registers) do not depend on whether a tile follows, the last one is loaded
+  // again: else the compiler would count only the loads that leave on every
+  // path, and wait for younger ones too.
+  template <int B>
+  __device__ __forceinline__ void two_steps(Stage& g, const Stream& st, f32x16& s, int k, int k1, int lo, int up, int blo,
+                                            int bup, float c, const int* ko, const int* vo, Lds& sh) {
+    const bool more = k + kTile < k1;
+    const int mid = k + kStepKeys;
+    constexpr int kHalf = kStepKeys * D * 2;   // bytes of a step's keys
+    float t;
+    g.load_v(st);
+    if (__builtin_expect(k < up, 1)) {
+      step(s, t, sh.k[B] + kHalf, sh.v[B], c, ko, vo);
+      unfinite(st, k, k + kTile, up, blo, sh.odd[B]);
+      if (__builtin_expect(mid < up, 1)) prepare(s, t, mid, lo, c);
+    }
+    if (__builtin_expect(more, 1)) {
+      g.store_k(sh.k[B ^ 1]);
+      wait_lds_barrier();
+    }
+    g.load_k(st, k + 2 * kTile, k1);
+    if (__builtin_expect(mid < up, 1)) {
+      step(s, t, sh.k[B ^ 1], sh.v[B] + kHalf, c, ko, vo);   // (the scores of a tile that is not there are not used)
+      unfinite(st, mid, k + kTile, up, blo, sh.odd[B]);
+      if (__builtin_expect(more && k + kTile < up, 1)) prepare(s, t, k + kTile, lo, c);
+    }
+    if (__builtin_expect(more, 1)) {
+      g.store_v(sh.v[B ^ 1]);
+      mend_v(sh.v[B ^ 1], sh.odd[B ^ 1], k + kTile, blo, bup);
       wait_lds_barrier();
     }
   }
@@ -293,7 +345,7 @@ struct Tiles {
   // Scores of the 32 keys at k, the largest of them in t: masks, and the
   // running maximum.
   __device__ __forceinline__ void prepare(f32x16& s, float t, int k, int lo, float c) {
-    if (__builtin_expect(k + kTile / 2 > lo, 0)) {
+    if (__builtin_expect(k + kStepKeys > lo, 0)) {
       const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[i] = k + 8 * (i >> 2) + 4 * g + (i & 3) < hi ? s[i] : -__builtin_inff();
@@ -355,13 +407,13 @@ struct Tiles {
     s = sn;
   }
 
-  // See unfinite_pair: keys [k, k + 32) of the tile at k0.
-  __device__ __forceinline__ void unfinite(const Stream& st, int k, int k0, int up, int blo, const uint32_t* odd) {
-    if (__builtin_expect(k0 + kTile <= blo, 1)) return;
+  // See unfinite_pair: keys [k, k + 32) of the tile that ends at `end`.
+  __device__ __forceinline__ void unfinite(const Stream& st, int k, int end, int up, int blo, const uint32_t* odd) {
+    if (__builtin_expect(end <= blo, 1)) return;
     if (__builtin_expect(!(odd[0] | odd[1] | odd[2] | odd[3]), 1)) return;
     const int g = (threadIdx.x & 63) >> 5;
 #pragma unroll 1
-    for (int key = k; key < min(k + kTile / 2, up); ++key) {
+    for (int key = k; key < min(k + kStepKeys, up); ++key) {
       const uint8_t* row = value_row(st, key) + (F8 ? 1 : 2) * 4 * g;
 #pragma unroll
       for (int d = 0; d < DT; ++d)

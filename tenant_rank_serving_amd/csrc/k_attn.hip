@@ -12,6 +12,8 @@
 //           and walks its prefix and its own keys; no partial sums.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "layer.h"
 
 namespace dc {
@@ -73,7 +75,7 @@ __device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, co
 // cover whole rows.
 template <int D, bool F8>
 __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, const Tiles<D, F8>& R, int row0, int h,
-                                          int slot, float vs, TilesLds<D>& sh) {
+                                          int slot, float vs, TilesLds<D, F8>& sh) {
   const int lane = threadIdx.x & 63, g = lane >> 5, i32 = lane & 31;
   const float l = R.l + __shfl_xor(R.l, 32);
   if (a.plan.direct) {
@@ -115,7 +117,7 @@ __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, con
 template <int D, bool F8>
 __device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages,
                                            Tiles<D, F8>& R, int blk0, int h, int c0,
-                                           int c1, float c, TilesLds<D>& sh) {
+                                           int c1, float c, TilesLds<D, F8>& sh) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row0 = blk0 + kTileRows * wave;
   const bool live = row0 < it.rows;
@@ -128,7 +130,7 @@ __device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, co
 
 template <int D, bool F8>
 __device__ __forceinline__ void tiles_block(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages, int blk0,
-                                            int h, int c0, int c1, int slot, TilesLds<D>& sh) {
+                                            int h, int c0, int c1, int slot, TilesLds<D, F8>& sh) {
   uint32_t flip;
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
   const int row0 = blk0 + kTileRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -146,7 +148,7 @@ template <int D, bool F8, int WO, int WP>
 __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int npre) {
   __shared__ union {
     KeysLds<D> keys;
-    TilesLds<WO == kByTiles || WP == kByTiles ? D : 8> tiles;
+    TilesLds<WO == kByTiles || WP == kByTiles ? D : 8, F8> tiles;
   } sh;
   const bool prefix = (int)blockIdx.x < npre;
   const int blk = prefix ? blockIdx.x : blockIdx.x - npre;
@@ -265,12 +267,23 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 }
 
 // Long queries.  Blocks of one (sequence, kv head) follow each other on one
-// XCD, the longest rows first.  PRE: some sequences have a prefix.
+// XCD, so that its L2 serves their keys, the longest rows first; the quarter
+// with the shortest rows of every sequence comes last and fills the end (187
+// us without that, 183 with; all sequences' longest rows first 219: their keys
+// do not fit).  PRE: some sequences have a prefix.
 template <int D, bool F8, bool PRE>
-__global__ void __launch_bounds__(64 * kWaves, 2) k_attn_rows(AttnArgs a) {
-  __shared__ TilesLds<D> sh;
+__global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs a) {
+  __shared__ TilesLds<D, F8> sh;
   const int xcd = blockIdx.x & 7, j8 = blockIdx.x >> 3;
-  const int p8 = a.plan.rbo_d.of(j8), rblk = a.plan.rbo - 1 - (j8 - p8 * a.plan.rbo);
+  const int light = a.plan.rbo >> 2, heavy = a.plan.rbo - light, h8 = (a.B * a.kv.heads + 7) / 8 * heavy;
+  int p8, rblk;
+  if (j8 < h8) {
+    p8 = a.plan.heavy_d.of(j8);
+    rblk = a.plan.rbo - 1 - (j8 - p8 * heavy);
+  } else {
+    p8 = a.plan.light_d.of(j8 - h8);
+    rblk = light - 1 - (j8 - h8 - p8 * light);
+  }
   const int pair = p8 * 8 + xcd;
   if (pair >= a.B * a.kv.heads) return;
   const int b = a.hkv_d.of(pair), h = pair - b * a.kv.heads;

@@ -256,6 +256,8 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   a.plan.rbo_d = dc::div_by(a.plan.rbo);
   a.plan.rbp_d = dc::div_by(a.plan.rbp);
   a.plan.so_d = dc::div_by(a.plan.so);
+  a.plan.heavy_d = dc::div_by(a.plan.rbo - (a.plan.rbo >> 2));
+  a.plan.light_d = dc::div_by(a.plan.rbo >> 2);
   a.plan.sp_d = dc::div_by(a.plan.sp);
   a.n = N;
   a.dim = kv->dim;

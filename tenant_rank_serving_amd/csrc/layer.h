@@ -58,6 +58,7 @@ struct AttnPlan {
   int32_t co, cp;     // keys of a split (multiples of 128)
   bool direct;        // one split in all: the outputs are written at once
   Div rbo_d, rbp_d, so_d, sp_d;
+  Div heavy_d, light_d;   // rows: row blocks of a sequence that come first, and last
   size_t o_off, ws;   // split form: partial sums at o_off of the workspace, its size
 };
 
