@@ -1,6 +1,7 @@
 // Entry points of the decoder-layer operators (paged key/value cache, 4-bit
 // backbone): argument checks on the host, then one launcher.  No allocation,
 // no synchronization.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -100,7 +101,7 @@ int64_t blocks_of(const dc::AttnPlan& p, int64_t B, int64_t G, int64_t heads) {
 
 namespace dc {
 
-constexpr int64_t kOwnBlocks = 512, kPrefixBlocks = 512;
+constexpr int64_t kOwnBlocks = 256, kPrefixBlocks = 512;
 
 AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, int32_t max_q, int32_t max_kv, int32_t G,
                    int32_t max_gq, int32_t max_pre) {
@@ -122,11 +123,9 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   auto blocks = [](int64_t rows, int32_t how) { return (int32_t)(how == 3 ? (rows + 127) / 128 : (rows + 16 * how - 1) / (16 * how)); };
   p.rbo = blocks(ro, p.wo);
   p.rbp = blocks(rg, p.wp);
-  // as many ranges as fill the card twice, each of 128 keys (a step a wave) or more
-  auto split = [](int64_t items, int64_t keys, int64_t want, int32_t* s, int32_t* c) {
-    if (items < 1) items = 1;
-    int64_t n = (want + items - 1) / items;
-    const int64_t most = (keys + 127) / 128;
+  // n ranges of keys for each item, of 128 (a step a wave) or more
+  auto split = [](int64_t n, int64_t keys, int64_t least, int32_t* s, int32_t* c) {
+    const int64_t most = (keys + least - 1) / least;
     if (n > most) n = most;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
@@ -135,9 +134,18 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
     *c = (int32_t)ch;
     *s = (int32_t)((keys + ch - 1) / ch);
   };
-  split((int64_t)B * hkv * p.rbo, max_kv, kOwnBlocks, &p.so, &p.co);
+  // few keys and few rows: one range, which needs no join (256 keys 8.5 -> 6.1
+  // us, 512: 8.4 -> 8.3, 640: 9.9 -> 10.6; 64 rows on 384 keys 11.8 -> 15.1)
+  const bool one = G == 0 && p.wo < 3 && max_kv <= 512;
+  const int64_t own = std::max<int64_t>((int64_t)B * hkv * p.rbo, 1), pre = std::max<int64_t>((int64_t)G * hkv * p.rbp, 1);
+  // a block a CU (4 x 131072 keys 260 us, with two 265; own keys behind a long
+  // prefix fill its end anyway)
+  split(one ? 1 : (kOwnBlocks + own - 1) / own, max_kv, 128, &p.so, &p.co);
   p.cp = 128;
-  if (G > 0) split((int64_t)G * hkv * p.rbp, max_pre, kPrefixBlocks, &p.sp, &p.cp);
+  // two a CU and no more, each of 256 keys or more when there are that many:
+  // every range costs its rows' partial sums (20 rows of 4 on 4000 keys, ranges
+  // of 128: 23.0 us, of 256: 19.2; on 400 keys 14.4 and 16.5)
+  if (G > 0) split(kPrefixBlocks / pre, max_pre, max_pre > 512 ? 256 : 128, &p.sp, &p.cp);
   if (p.sp == 0 && p.so <= 1) {
     p.so = 1;
     p.direct = true;
