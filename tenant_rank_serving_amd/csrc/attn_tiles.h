@@ -17,6 +17,13 @@
 //       value_swizzle).  bf16 keys go straight to LDS (global_load_lds, no
 //       registers; the lanes choose the permuted pieces); e4m3 codes pass
 //       through registers and are converted, once a block.
+// Measured, 8 prompts of up to 2048 tokens, 32 heads on 8, bf16: 181 us, 845
+// TFLOP/s.  In the middle of a block the matrix cores are busy 68 % of the
+// time, as in a large library product, at a clock that the power limit sets
+// (1.83 GHz; with two blocks a CU 58 % at 1.93, the same time); the rest is a
+// block's first loads and its output (14000 of 60000 cycles) and the last
+// blocks.  Without any exponentials it would take 160 us, without reading LDS
+// 173.
 #pragma once
 
 __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {

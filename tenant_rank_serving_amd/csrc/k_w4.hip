@@ -7,7 +7,7 @@
 //   sum_k (q_k - z) x_k = sum_k (128 + q_k) x_k - (128 + z) sum_k x_k.
 // The sums of x come from the matrix core too, against a tile of ones (the
 // same for every row).  What the 128 adds cancels to 2^-24 * 128 of the sum of
-// |x|: 2^-17 of it, below the output's rounding of 2^-9.
+// |x|: 2^-17 of it, below the output's rounding of 2^-8.
 #include <hip/hip_runtime.h>
 
 #include "layer.h"
@@ -188,10 +188,12 @@ void go(const W4Args& a) {
 // when all read (x comes from L2 again in every block), so the time is that
 // of what the fullest CU reads: RT row tiles of the matrix (8.5 bytes an
 // input with the scales) and the tokens' x (2 bytes an input each), for each
-// round of 256 blocks.  Measured, us, all 10 tiles timed: 4096 x 4096 with 64 tokens (1,1) 18.6,
-// (1,4) 17.1, (4,1) 8.8; 11008 x 4096 with 16 (1,1) 14.7, (2,1) 11.6, (3,1)
-// 8.2, (4,1) 9.0, with 64 (4,4) 21.5, (3,4) 20.3, (6,2) 15.6; 4096 x 14336
-// with 1 (1,1) 10.3, (2,1) 12.6.
+// round of 256 blocks.  Measured, us, all 10 tiles timed: 4096 x 4096 with 64
+// tokens (1,1) 18.6, (1,4) 17.1, (4,1) 8.8; 11008 x 4096 with 16 (1,1) 14.7,
+// (2,1) 11.6, (3,1) 8.2, (4,1) 9.0, with 64 (4,4) 21.5, (3,4) 20.3, (6,2)
+// 15.1; 4096 x 14336 with 1 (1,1) 10.3, (2,1) 12.6.  4096 x 14336 with 7 tokens
+// takes 10.6 however many groups are loaded ahead (2 to 8), with 8 waves or 16,
+// and wherever a block begins in x.
 int launch_w4(const W4Args& a) {
   constexpr int kTiles[][2] = {{1, 1}, {2, 1}, {3, 1}, {4, 1}, {6, 1}, {8, 1}, {2, 2}, {4, 2}, {6, 2}, {8, 2}};
   int best = 0;
