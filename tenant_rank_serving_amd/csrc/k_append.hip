@@ -152,8 +152,10 @@ __global__ void __launch_bounds__(kThreads) k_append(AppendArgs a, int per) {
 int launch_append(const AppendArgs& a) {
   const int units = (a.hq + 2 * a.kv.heads) * (a.dim / 16);
   // few tokens: one unit a thread, so that the whole call is in flight at
-  // once; many: four, so that a block shares its token's angles
-  const bool few = a.n < 512;
+  // once; many: four, so that a block shares its token's angles (us, one / four:
+  // 64 tokens of 48 heads 3.5 / 4.0, 1024 7.0 / 7.4, 4096 19.8 / 19.3; 512 of 120
+  // heads 7.6 / 8.7, 2048 29.6 / 28.7)
+  const bool few = a.n <= 1024;
   const int per = few ? kThreads : kThreads * 4;
   const dim3 g((unsigned)a.n, (unsigned)((units + per - 1) / per));
   hipStream_t st = reinterpret_cast<hipStream_t>(a.stream);

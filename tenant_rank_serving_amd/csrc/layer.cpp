@@ -108,15 +108,20 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   AttnPlan p{};
   const int64_t ro = (int64_t)max_q * gq, rg = (int64_t)max_gq * gq;   // query rows of a sequence, of a group
   if (max_pre == 0 || max_gq == 0) G = 0;
-  // long queries: enough blocks of 128 rows to fill the card
-  const int64_t rb = (ro + 127) / 128;
-  if (ro > 32 && (int64_t)B * hkv * rb >= 256) {
+  // long queries: enough blocks of 128 rows to fill the card, or to get through
+  // few keys before split ones are joined (us, in rows / split: 256 blocks x
+  // 4096 keys 108 / 110; 512 x 8192 263 / 274; 128 x 512 18.7 / 26.6, x 1024
+  // 31.6 / 33.5, x 2048 56 / 47; 64 x 512 18.3 / 21.1, x 1024 31 / 25)
+  const int64_t rb = (ro + 127) / 128, all = (int64_t)B * hkv * rb;
+  if (ro > 32 && (all >= 256 || (all >= 64 && (int64_t)max_kv + (G > 0 ? max_pre : 0) <= 8 * all))) {
     p.rows = true;
     p.rbo = (int32_t)rb;
     p.co = p.cp = 128;
     p.direct = true;
     return p;
   }
+  // us, 16 rows / 32 / 128 at a time: 8 x 4000 e4m3 keys with 16 rows 16.6 / 18.3
+  // / -, with 32 rows 19.8 by 32, 31.5 by 128; with 48 rows 36.6 by 32 twice, 37.8
   auto walk = [](int64_t rows) { return rows <= 16 ? 1 : (rows <= 32 ? 2 : 3); };
   p.wo = walk(ro);
   p.wp = walk(rg) > p.wo ? walk(rg) : p.wo;
@@ -170,7 +175,7 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
   if (st != DC_OK) return st;
   if (N < 0 || q_heads < 0) return DC_ERR_INVALID_ARG;
   const int64_t qc = (int64_t)q_heads * kv->dim, kc = (int64_t)kv->heads * kv->dim;
-  if ((qc + 2 * kc) / 16 > INT32_MAX / 2) return DC_ERR_UNSUPPORTED;
+  if ((qc + 2 * kc) / 16 > 65535 * 256) return DC_ERR_UNSUPPORTED;   // a launch's blocks along y
   if (rope) {
     if (rope->rot < 16 || rope->rot > kv->dim || rope->rot % 16) return DC_ERR_SHAPE;
     if (!rope->inv_freq || !pos) return DC_ERR_INVALID_ARG;

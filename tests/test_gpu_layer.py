@@ -779,3 +779,11 @@ def test_w4_captured_and_what_is_not_finite(t_):
     g.replay()
     t.cuda.synchronize()
     assert not t.isfinite(y[0]).any() and np.array_equal(host_bits(y[1:t_]), host_bits(want[1:]))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attention_of_a_single_prompt(kv):
+    """64 blocks of 128 rows: few keys are walked whole, more are split."""
+    for own in (256, 900):
+        note("attention, one prompt", own, kv)
+        Case(50 + own, nq=[256], kv_len=[own], groups=[0], prefix=[], hq=32, hkv=8, dim=64, page=16, kv=kv).check()

@@ -208,3 +208,7 @@ def test_attention_scales_out_of_range(L, scale):
 
 def test_attention_scales_at_the_ends(L):
     assert attend(L, scale=1.2e-38) == E.DC_OK and attend(L, scale=2.3e38) == E.DC_OK
+
+
+def test_append_of_more_heads_than_a_launch_takes(L):
+    assert append(L, hq=1 << 21, qs=1 << 28, qos=1 << 28, n=1, q=1 << 40, qo=1 << 42, k=1 << 43, v=1 << 44) == E.DC_ERR_UNSUPPORTED
