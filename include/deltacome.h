@@ -674,6 +674,10 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
  *             own keys, of query tokens of a group, of prefix keys
  * Query token j of the n of sequence b sees its group's whole prefix and the
  * own keys 0 .. kv_len[b] - n + j.
+ * The bounds choose one form for the whole call: with long queries (more than
+ * 32 rows of a kv head, in 64 blocks of 128 or more) a sequence's keys are read
+ * by the blocks of its rows alone, so single tokens with many keys are better
+ * off in a call of their own, beside the one for the prompts.
  */
 typedef struct dc_attn_batch {
   int32_t seqs, max_q, max_kv, seq_pages;

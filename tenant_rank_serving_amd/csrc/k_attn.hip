@@ -121,7 +121,7 @@ __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, con
 // One walk of a block's rows over keys [c0, c1) of an item.
 template <int D, bool F8>
 __device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages,
-                                           Tiles<D, F8>& R, int blk0, int h, int c0,
+                                           Tiles<D, F8>& R, int blk0, int c0,
                                            int c1, float c, TilesLds<D, F8>& sh) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row0 = blk0 + kTileRows * wave;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void tiles_block(const AttnArgs& a, const Item& it, c
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, it, row0, h, flip);
-  tiles_walk<D, F8>(a, it, st, pages, R, blk0, h, c0, c1, c, sh);
+  tiles_walk<D, F8>(a, it, st, pages, R, blk0, c0, c1, c, sh);
   put_tiles<D, F8>(a, it, R, row0, h, slot, vs, sh);
 }
 
@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs 
     const Stream ps = prefix_stream(a, h, max(gr, 0));
     Pages pp;
     pp.fill(ps, 0);
-    tiles_walk<D, F8>(a, it, ps, pp, R, blk0, h, 0, it.len, c, sh);
+    tiles_walk<D, F8>(a, it, ps, pp, R, blk0, 0, it.len, c, sh);
   }
-  tiles_walk<D, F8>(a, own, st, pages, R, blk0, h, 0, own.len, c, sh);
+  tiles_walk<D, F8>(a, own, st, pages, R, blk0, 0, own.len, c, sh);
   put_tiles<D, F8>(a, own, R, row0, h, 0, vs, sh);
 }
 
