@@ -702,7 +702,9 @@ typedef struct dc_attn_batch {
  *             aligned; holds nothing between calls, so calls that follow each
  *             other may share one, and calls that may run at once may not
  * A row that sees no key gets zeros.  What lies in slots that a row does not
- * see (infinities and NaN included) does not reach it.
+ * see (infinities and NaN included) does not reach it; an infinite value that
+ * it sees makes its result infinite, however small the weight (two of different
+ * signs, or a NaN, make NaN).  Blocks that meet such values take more time.
  * Arithmetic: bf16 products with fp32 sums; the weights enter the second
  * product as bf16 (as two bf16 pieces where at most 16 rows share the keys),
  * and the row's sum is taken of the weights as they entered; joined in a fixed

@@ -126,6 +126,46 @@ template <bool F8> __device__ __forceinline__ f32x2 unfinite_pair(const uint8_t*
   const float a = lo_f(w), b = hi_f(w);
   return f32x2{seen && !__builtin_isfinite(a) ? a : 0.f, seen && !__builtin_isfinite(b) ? b : 0.f};
 }
+// Where every row sees every key of a step, values go into the products as they
+// are.  An infinite one can then end as NaN: times a weight that is too small
+// for its type, or times the second piece of a weight, which may be zero or
+// negative.  So a block whose results are not all finite, though its rows'
+// weights are, does its work once more and treats every step as one with masks
+// (finite data pays for looking at the results only).  A row's sums of finite
+// values are the same both times, bit for bit.
+
+// The factor of sums of values whose maximum has moved.  Where it is zero (an
+// exponential is, or 2^-126 or more), infinite sums stay and finite ones vanish
+// all the same, as 2^-126 times 2^-126 of them.
+struct Factor {
+  float f, g;
+  explicit __device__ __forceinline__ Factor(float x) : f(fmaxf(x, 0x1p-126f)), g(x < 0x1p-126f ? 0x1p-126f : 1.f) {}
+  __device__ __forceinline__ float of(float x) const { return x * f * g; }
+};
+
+// The block's arguments, number and thread, taken anew each time it does its work:
+// what is derived from them would else be kept for a second time and cost
+// registers in the walk.
+__device__ __forceinline__ const AttnArgs& args_anew() {
+  auto p = (const __attribute__((address_space(4))) AttnArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnArgs*)p;
+}
+__device__ __forceinline__ int block_anew() {
+  int b = blockIdx.x;
+  asm volatile("" : "+s"(b));
+  return b;
+}
+// (and both times by the same code)
+__device__ __forceinline__ bool one_code(int again) {
+  asm volatile("" : "+s"(again));
+  return again != 0;
+}
+__device__ __forceinline__ int thread_anew() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
 
 // The query rows of a sequence (of a group) for one kv head: row r is token
 // t0 + r / gq, query head r % gq of the kv head's.

@@ -42,7 +42,7 @@ struct Keys {
   int32_t hi[N];   // keys the lane's row of a tile sees: [0, hi)
 
   __device__ __forceinline__ void start(const AttnArgs& a, const Item& it, int row0, int h, uint32_t flip) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const int lane = thread_anew() & 63, g = lane >> 4;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int row = min(row0 + 16 * n + (lane & 15), it.rows - 1);   // past the last row: the last one again
@@ -61,6 +61,21 @@ struct Keys {
       l[n] = f32x4{0.f, 0.f, 0.f, 0.f};
       m[n] = kLow;
     }
+  }
+
+  // Whether some result of the wave is not finite though its row's weights are.
+  __device__ __forceinline__ bool unfinite_results() const {
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};   // NaN as soon as one is not finite
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z[r] = __builtin_fmaf(o[n][j][r], 0.f, z[r]);
+      bad |= (z[0] + z[1]) + (z[2] + z[3]) != 0.f && __builtin_isfinite(l[n][0]);
+    }
+    return __builtin_amdgcn_ballot_w64(bad) != 0;
   }
 
   static constexpr int KB = F8 ? 1 : 2;                // bytes of an element
@@ -177,10 +192,11 @@ struct Keys {
         m[n] = mn;
 #pragma unroll
         for (int r = 0; r < 4; ++r) l[n][r] *= f;
+        const Factor k(f);
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[n][j][r] *= f;
+          for (int r = 0; r < 4; ++r) o[n][j][r] = k.of(o[n][j][r]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(x[e] * c - m[n]);
@@ -229,16 +245,22 @@ struct Keys {
 
 // The four waves' sums of one block (they walked different keys for the same
 // rows) joined in LDS, 16 rows at a time, and handed to `put`, D/16
-// consecutive elements a thread.
+// consecutive elements a thread.  With `look`, results that are not finite (see
+// Factor) are not joined: true.
 template <int D>
 struct KeysLds {
+  uint32_t odd[kWaves];
   float ml[kWaves][32][2];
   alignas(16) float o[kWaves][16][D + 4];
 };
 template <int D, bool F8, int N, class Put>
-__device__ __forceinline__ void join(const Keys<D, F8, N>& R, KeysLds<D>& sh, Put put) {
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, i16 = lane & 15;
+__device__ __forceinline__ bool join(const Keys<D, F8, N>& R, KeysLds<D>& sh, bool look, Put put) {
+  const int tid = thread_anew(), wave = tid >> 6, lane = tid & 63, g = lane >> 4, i16 = lane & 15;
   constexpr int J = D / 16;
+  if constexpr (!F8) {
+    const bool odd = R.unfinite_results();
+    if (lane == 0) sh.odd[wave] = odd;
+  }
   if (g == 0) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -257,6 +279,11 @@ __device__ __forceinline__ void join(const Keys<D, F8, N>& R, KeysLds<D>& sh, Pu
         *reinterpret_cast<f32x4*>(&sh.o[wave][i16][J * (4 * g + r) + j]) =
             f32x4{R.o[n][j][r], R.o[n][j + 1][r], R.o[n][j + 2][r], R.o[n][j + 3][r]};
     __syncthreads();
+    if (!F8 && n == 0 && look &&
+        __builtin_expect(__builtin_amdgcn_readfirstlane(sh.odd[0] | sh.odd[1] | sh.odd[2] | sh.odd[3]) != 0, 0)) {
+      __syncthreads();   // read before the next time writes there
+      return true;
+    }
     const int row = tid >> 4, e = (tid & 15) * J;
     float m = kLow, l = 0.f, x[J];
 #pragma unroll
@@ -267,9 +294,11 @@ __device__ __forceinline__ void join(const Keys<D, F8, N>& R, KeysLds<D>& sh, Pu
     for (int w = 0; w < kWaves; ++w) {
       const float f = __builtin_amdgcn_exp2f(sh.ml[w][16 * n + row][0] - m);
       l += sh.ml[w][16 * n + row][1] * f;
+      const Factor k(f);
 #pragma unroll
-      for (int j = 0; j < J; ++j) x[j] += sh.o[w][row][e + j] * f;
+      for (int j = 0; j < J; ++j) x[j] += k.of(sh.o[w][row][e + j]);
     }
     put(16 * n + row, e, m, l, x);
   }
+  return false;
 }

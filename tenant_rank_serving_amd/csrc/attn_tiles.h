@@ -71,7 +71,7 @@ struct Tiles {
   }
   // row0: the wave's first row
   __device__ __forceinline__ void load_q(const AttnArgs& a, const Item& it, int row0, int h, uint32_t flip) {
-    const int lane = threadIdx.x & 63;
+    const int lane = thread_anew() & 63;
     const int row = min(row0 + (lane & 31), it.rows - 1);   // past the last row: the last one again
     const int tok = a.gq_d.of(row), hh = row - tok * a.gq;
     const uint16_t* p = a.q + (int64_t)(it.t0 + tok) * a.qs + (int64_t)(h * a.gq + hh) * D + 8 * (lane >> 5);
@@ -80,6 +80,22 @@ struct Tiles {
       q[i] = *reinterpret_cast<const uint4*>(p + 16 * i);
       if constexpr (F8) q[i].x ^= flip, q[i].y ^= flip, q[i].z ^= flip, q[i].w ^= flip;
     }
+  }
+
+  // Whether some result of the block is not finite though its row's weights
+  // are; every wave has left the walk.
+  __device__ __forceinline__ bool unfinite_results(Lds& sh) const {
+    f32x4 z = f32x4{0.f, 0.f, 0.f, 0.f};   // NaN as soon as one is not finite
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) z[i & 3] = __builtin_fmaf(o[d][i], 0.f, z[i & 3]);
+    const bool found = __builtin_amdgcn_ballot_w64((z[0] + z[1]) + (z[2] + z[3]) != 0.f && __builtin_isfinite(l + __shfl_xor(l, 32))) != 0;
+    if ((threadIdx.x & 63) == 0) sh.odd[0][threadIdx.x >> 6] = found;
+    wait_lds_barrier();
+    const bool any = __builtin_amdgcn_readfirstlane(sh.odd[0][0] | sh.odd[0][1] | sh.odd[0][2] | sh.odd[0][3]) != 0;
+    if (__builtin_expect(any, 0)) wait_lds_barrier();   // read before the next time writes there
+    return any;
   }
 
   // Keys [k0, k1) of the stream (k0 a multiple of 64, its page in `pages`) for
@@ -95,7 +111,7 @@ struct Tiles {
                                        int bup, float c, bool live, Lds& sh) {
     k1 = min(k1, bup);
     if (k0 >= k1) return;
-    const int lane = threadIdx.x & 63, half = lane >> 5, i32 = lane & 31;
+    const int lane = thread_anew() & 63, half = lane >> 5, i32 = lane & 31;
     int ko[KS], vo[DT];
 #pragma unroll
     for (int i = 0; i < KS; ++i) ko[i] = i32 * (D * 2) + (((2 * i + half) ^ key_swizzle<D>(i32)) * 16);
@@ -179,7 +195,7 @@ struct Tiles {
     int wave, ko[KL], vo;   // the lane's offsets in the keys' rows
     uint32_t at;            // LDS address of the wave's part of the first tile of keys
     __device__ __forceinline__ Direct(const Stream& st, const Pages& p, const Lds& sh) : pages(p) {
-      const int lane = threadIdx.x & 63;
+      const int lane = thread_anew() & 63;
       wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
       at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)&sh.k[0][0] + wave * (KW * D * 2);
       const int key = lane / KP, pos = lane % KP;   // LDS takes 16 bytes a lane, in the order of the lanes
@@ -256,7 +272,7 @@ struct Tiles {
   // now, those that are not finite.  The wave's own keys, once they are in LDS.
   static __device__ __forceinline__ void mend_v(uint8_t* lds, uint32_t* odd, int k, int blo, int bup) {
     if (__builtin_expect(k + kTile <= blo, 1)) return;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = thread_anew(), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     if constexpr (F8) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (one wave wrote, other lanes read)
     uint32_t any = 0;
 #pragma unroll
@@ -365,10 +381,11 @@ struct Tiles {
       const float f = __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       l *= f;
+      const Factor k(f);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+        for (int i = 0; i < 16; ++i) o[d][i] = k.of(o[d][i]);
     }
   }
 
@@ -418,7 +435,7 @@ struct Tiles {
   __device__ __forceinline__ void unfinite(const Stream& st, int k, int end, int up, int blo, const uint32_t* odd) {
     if (__builtin_expect(end <= blo, 1)) return;
     if (__builtin_expect(!(odd[0] | odd[1] | odd[2] | odd[3]), 1)) return;
-    const int g = (threadIdx.x & 63) >> 5;
+    const int g = (thread_anew() & 63) >> 5;
 #pragma unroll 1
     for (int key = k; key < min(k + kStepKeys, up); ++key) {
       const uint8_t* row = value_row(st, key) + (F8 ? 1 : 2) * 4 * g;

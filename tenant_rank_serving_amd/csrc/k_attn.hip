@@ -42,10 +42,12 @@ __device__ __forceinline__ Out out_of(const AttnArgs& a, const Item& it, int row
   return o;
 }
 
+// A block's work; `again`: every step is treated as one with masks.  True: it
+// has to be done again (see Factor).
 template <int D, bool F8, int N>
-__device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, const Stream& st, Pages& pages, int row0, int h,
-                                           int c0, int c1, int slot, KeysLds<D>& sh) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ bool keys_block(const AttnArgs& a, const Item& it, const Stream& st, Pages& pages, int row0, int h,
+                                           int c0, int c1, int slot, bool again, KeysLds<D>& sh) {
+  const int wave = __builtin_amdgcn_readfirstlane(thread_anew() >> 6);
   const int last = min(row0 + 16 * N, it.rows) - 1;
   const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(last));
   const int w0 = c0 + 32 * wave, w1 = min(c1, up);
@@ -59,9 +61,9 @@ __device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, co
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
   Keys<D, F8, N> R;
   R.start(a, it, row0, h, flip);
-  R.walk(st, g, pages, w0, w1, lo, up, c);
+  R.walk(st, g, pages, w0, w1, again ? 0 : lo, up, c);
   constexpr int J = D / 16;
-  join<D, F8, N>(R, sh, [&](int row, int e, float m, float l, const float* x) __attribute__((always_inline)) {
+  return join<D, F8, N>(R, sh, !again, [&](int row, int e, float m, float l, const float* x) __attribute__((always_inline)) {
     if (row0 + row >= it.rows) return;
     const Out w = out_of<D>(a, it, row0 + row, h, slot);
     if (a.plan.direct) {
@@ -81,12 +83,12 @@ __device__ __forceinline__ void keys_block(const AttnArgs& a, const Item& it, co
 template <int D, bool F8>
 __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, const Tiles<D, F8>& R, int row0, int h,
                                           int slot, float vs, TilesLds<D, F8>& sh) {
-  const int lane = threadIdx.x & 63, g = lane >> 5, i32 = lane & 31;
+  const int tid = thread_anew(), lane = tid & 63, g = lane >> 5, i32 = lane & 31;
   const float l = R.l + __shfl_xor(R.l, 32);
   if (a.plan.direct) {
     constexpr int kRow = D * 2 + 16;   // of LDS: neighbouring rows in other banks
     static_assert(kWaves * kTileRows * kRow <= (int)sizeof(sh.k) + (int)sizeof(sh.v), "the rows fit over the tiles");
-    uint8_t* mine = &sh.k[0][0] + (threadIdx.x >> 6) * (kTileRows * kRow);
+    uint8_t* mine = &sh.k[0][0] + (tid >> 6) * (kTileRows * kRow);
     const float f = l == 0.f ? 0.f : vs / l;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -121,42 +123,45 @@ __device__ __forceinline__ void put_tiles(const AttnArgs& a, const Item& it, con
 // One walk of a block's rows over keys [c0, c1) of an item.
 template <int D, bool F8>
 __device__ __forceinline__ void tiles_walk(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages,
-                                           Tiles<D, F8>& R, int blk0, int c0,
-                                           int c1, float c, TilesLds<D, F8>& sh) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+                                           Tiles<D, F8>& R, int blk0, int c0, int c1, bool again, float c,
+                                           TilesLds<D, F8>& sh) {
+  const int wave = __builtin_amdgcn_readfirstlane(thread_anew() >> 6);
   const int row0 = blk0 + kTileRows * wave;
   const bool live = row0 < it.rows;
   const int blast = min(blk0 + kBlockRows, it.rows) - 1, wlast = min(row0 + kTileRows, it.rows) - 1;
   const int blo = it.sees(a.gq_d.of(blk0)), bup = it.sees(a.gq_d.of(blast));
   const int lo = it.sees(a.gq_d.of(row0)), up = it.sees(a.gq_d.of(max(wlast, 0)));
-  R.hi = it.sees(a.gq_d.of(min(row0 + (int)(threadIdx.x & 31), it.rows - 1)));
-  R.walk(st, pages, c0, c1, lo, up, blo, bup, c, live, sh);
+  R.hi = it.sees(a.gq_d.of(min(row0 + (thread_anew() & 31), it.rows - 1)));
+  R.walk(st, pages, c0, c1, lo, up, again ? 0 : blo, bup, c, live, sh);
 }
 
 template <int D, bool F8>
-__device__ __forceinline__ void tiles_block(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages, int blk0,
-                                            int h, int c0, int c1, int slot, TilesLds<D, F8>& sh) {
+__device__ __forceinline__ bool tiles_block(const AttnArgs& a, const Item& it, const Stream& st, const Pages& pages, int blk0,
+                                            int h, int c0, int c1, int slot, bool again, TilesLds<D, F8>& sh) {
   uint32_t flip;
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
-  const int row0 = blk0 + kTileRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = blk0 + kTileRows * __builtin_amdgcn_readfirstlane(thread_anew() >> 6);
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, it, row0, h, flip);
-  tiles_walk<D, F8>(a, it, st, pages, R, blk0, c0, c1, c, sh);
+  tiles_walk<D, F8>(a, it, st, pages, R, blk0, c0, c1, again, c, sh);
+  if (!F8 && !again && __builtin_expect(R.unfinite_results(sh), 0)) return true;
   put_tiles<D, F8>(a, it, R, row0, h, slot, vs, sh);
+  return false;
 }
 
 // Split form.  WO, WP: how own keys and prefixes are walked, by Keys of 16 or
 // 32 rows (1, 2) or by Tiles (3).
 constexpr int kByTiles = 3;
 template <int D, bool F8, int WO, int WP>
-__global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int npre) {
-  __shared__ union {
-    KeysLds<D> keys;
-    TilesLds<WO == kByTiles || WP == kByTiles ? D : 8, F8> tiles;
-  } sh;
-  const bool prefix = (int)blockIdx.x < npre;
-  const int blk = prefix ? blockIdx.x : blockIdx.x - npre;
+union SplitLds {
+  KeysLds<D> keys;
+  TilesLds<WO == kByTiles || WP == kByTiles ? D : 8, F8> tiles;
+};
+template <int D, bool F8, int WO, int WP>
+__device__ __forceinline__ bool split_block(const AttnArgs& a, int npre, int block, bool again, SplitLds<D, F8, WO, WP>& sh) {
+  const bool prefix = block < npre;
+  const int blk = prefix ? block : block - npre;
   const int rb = prefix ? a.plan.rbp : a.plan.rbo, ns = prefix ? a.plan.sp : a.plan.so;
   const int chunk = prefix ? a.plan.cp : a.plan.co;
   int u = (prefix ? a.plan.rbp_d : a.plan.rbo_d).of(blk);
@@ -171,13 +176,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int n
   const Item it = prefix ? prefix_item(a, b) : own_item(a, b);
   const int how = prefix ? WP : WO;
   const int row0 = r * (how == kByTiles ? kBlockRows : 16 * how);
-  if (row0 >= it.rows) return;
+  if (row0 >= it.rows) return false;
   const int c1 = min(it.len, c0 + chunk);
-  if (c0 >= c1 && !a.plan.direct) return;   // the join knows that it holds nothing
+  if (c0 >= c1 && !a.plan.direct) return false;   // the join knows that it holds nothing
   const int slot = prefix ? s : a.plan.sp + s;
 #define DC_WALK(W_)                                                                                 \
-  if constexpr (W_ == kByTiles) tiles_block<D, F8>(a, it, st, pages, row0, h, c0, c1, slot, sh.tiles); \
-  else keys_block<D, F8, W_>(a, it, st, pages, row0, h, c0, c1, slot, sh.keys);
+  if constexpr (W_ == kByTiles) return tiles_block<D, F8>(a, it, st, pages, row0, h, c0, c1, slot, again, sh.tiles); \
+  else return keys_block<D, F8, W_>(a, it, st, pages, row0, h, c0, c1, slot, again, sh.keys);
   if constexpr (WO == WP) {
     DC_WALK(WO)
   } else if (prefix) {
@@ -186,6 +191,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) k_attn_split(AttnArgs a, int n
     DC_WALK(WO)
   }
 #undef DC_WALK
+}
+// (three blocks a CU where the tiles of bf16 leave room for them)
+template <int D, bool F8, int WO, int WP>
+__global__ void __launch_bounds__(64 * kWaves, !F8 && WO != 2 && WP == kByTiles ? 3 : 2) k_attn_split(AttnArgs, int npre) {
+  __shared__ SplitLds<D, F8, WO, WP> sh;
+  for (int again = 0; split_block<D, F8, WO, WP>(args_anew(), npre, block_anew(), one_code(again), sh) && !F8;) again = 1;
 }
 
 // Joins the splits of a row: one wave a row.  Everything that does not depend
@@ -256,9 +267,9 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int s = s0 + i * P + lane / L;
-      const float w = s < 64 ? __shfl(wa, s & 63) : __shfl(wb, s & 63);
+      const Factor w(s < 64 ? __shfl(wa, s & 63) : __shfl(wb, s & 63));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] += held(s) ? o[i][j] * w : 0.f;
+      for (int j = 0; j < 4; ++j) x[j] += held(s) ? w.of(o[i][j]) : 0.f;
     }
   }
 #pragma unroll
@@ -277,9 +288,8 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
 // us without that, 183 with; all sequences' longest rows first 219: their keys
 // do not fit).  PRE: some sequences have a prefix.
 template <int D, bool F8, bool PRE>
-__global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs a) {
-  __shared__ TilesLds<D, F8> sh;
-  const int xcd = blockIdx.x & 7, j8 = blockIdx.x >> 3;
+__device__ __forceinline__ bool rows_block(const AttnArgs& a, int block, bool again, TilesLds<D, F8>& sh) {
+  const int xcd = block & 7, j8 = block >> 3;
   const int light = a.plan.rbo >> 2, heavy = a.plan.rbo - light, h8 = (a.B * a.kv.heads + 7) / 8 * heavy;
   int p8, rblk;
   if (j8 < h8) {
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs 
     rblk = light - 1 - (j8 - h8 - p8 * light);
   }
   const int pair = p8 * 8 + xcd;
-  if (pair >= a.B * a.kv.heads) return;
+  if (pair >= a.B * a.kv.heads) return false;
   const int b = a.hkv_d.of(pair), h = pair - b * a.kv.heads;
   // the page numbers are on their way while the lengths are read
   const Stream st = own_stream(a, h, b);
@@ -298,10 +308,10 @@ __global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs 
   pages.fill(st, 0);
   const Item own = own_item(a, b);
   const int blk0 = rblk * kBlockRows;
-  if (blk0 >= own.rows) return;
+  if (blk0 >= own.rows) return false;
   uint32_t flip;
   const float c = score_factor<F8>(a, h, &flip), vs = value_scale<F8>(a, h);
-  const int row0 = blk0 + kTileRows * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = blk0 + kTileRows * __builtin_amdgcn_readfirstlane(thread_anew() >> 6);
   Tiles<D, F8> R;
   R.clear();
   R.load_q(a, own, row0, h, flip);
@@ -313,10 +323,17 @@ __global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs 
     const Stream ps = prefix_stream(a, h, max(gr, 0));
     Pages pp;
     pp.fill(ps, 0);
-    tiles_walk<D, F8>(a, it, ps, pp, R, blk0, 0, it.len, c, sh);
+    tiles_walk<D, F8>(a, it, ps, pp, R, blk0, 0, it.len, again, c, sh);
   }
-  tiles_walk<D, F8>(a, own, st, pages, R, blk0, 0, own.len, c, sh);
+  tiles_walk<D, F8>(a, own, st, pages, R, blk0, 0, own.len, again, c, sh);
+  if (!F8 && !again && __builtin_expect(R.unfinite_results(sh), 0)) return true;
   put_tiles<D, F8>(a, own, R, row0, h, 0, vs, sh);
+  return false;
+}
+template <int D, bool F8, bool PRE>
+__global__ void __launch_bounds__(64 * kWaves, F8 ? 2 : 3) k_attn_rows(AttnArgs) {
+  __shared__ TilesLds<D, F8> sh;
+  for (int again = 0; rows_block<D, F8, PRE>(args_anew(), block_anew(), one_code(again), sh) && !F8;) again = 1;
 }
 
 template <int D, bool F8>

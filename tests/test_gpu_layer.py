@@ -787,3 +787,60 @@ def test_attention_of_a_single_prompt(kv):
     for own in (256, 900):
         note("attention, one prompt", own, kv)
         Case(50 + own, nq=[256], kv_len=[own], groups=[0], prefix=[], hq=32, hkv=8, dim=64, page=16, kv=kv).check()
+
+
+# 4 rows of a kv head; 20; 40: each walk of the keys.  With large scores most weights are 0 in 32 bits and the running
+# maximum jumps by more than 2^149.
+@pytest.mark.parametrize("std", [1.0, 12.0])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gq", [4, 20, 40])
+def test_attention_every_visible_infinity(gq, dim, std):
+    """An infinite value that a row sees makes its result infinite (every weight is positive), whichever key it is, the
+    heaviest and the lightest included; two of different signs make NaN.  The other elements stay as they are."""
+    note("attention, every visible infinity", gq, dim, std)
+    n, keys, hkv, page = 71, 70, 2, 16
+    c = Case(gq + dim, nq=[1] * n, kv_len=[keys] * n, groups=[0], prefix=[], hq=gq * hkv, hkv=hkv, dim=dim, page=page, kv="bf16", std=std)
+    at = lambda b, i: (c.tables[b][i // page], 0, i % page, 7 * b % dim)  # noqa: E731
+    spots = [(b, b, 0x7F80 if b % 2 else 0xFF80) for b in range(keys)] + [(keys, 1, 0x7F80), (keys, 40, 0xFF80)]
+    for b, i, _ in spots:
+        c.pool.v[at(b, i)] = 0
+    y, tol = c.reference()
+    for b, i, w in spots:
+        c.pool.v[at(b, i)] = w
+    c.reload()
+    got = vals(c.run())
+    rest = np.ones(got.shape, bool)
+    for b in range(n):
+        e = 7 * b % dim
+        rest[b, :gq, e] = False
+        want = np.nan if b == keys else np.inf if b % 2 else -np.inf
+        assert np.array_equal(got[b, :gq, e], np.full(gq, want), equal_nan=True), (b, got[b, :gq, e])
+    assert (np.abs(got - y) <= tol)[rest].all()
+
+
+@pytest.mark.parametrize("prefix", [0, 150])
+@pytest.mark.parametrize("std", [1.0, 12.0])
+def test_attention_visible_infinities_of_a_prompt(prefix, std):
+    """A block that walks all keys of its rows: an infinite value reaches every token that sees it, own key or prefix, and
+    nothing else."""
+    note("attention, visible infinities of a prompt", prefix, std)
+    heads, n, own, page, dim = 64, 70, 200, 16, 64
+    c = Case(prefix + 3, nq=[n], kv_len=[own], groups=[0, 1] if prefix else [0], prefix=[prefix] if prefix else [], hq=heads, hkv=heads,
+             dim=dim, page=page, kv="bf16", std=std)
+    spots = []                                   # head, key (of the prefix and the own keys behind it), element
+    for h in range(heads):
+        i = h * 5 % (prefix + own)
+        t, j = (c.ptables[0], i) if i < prefix else (c.tables[0], i - prefix)
+        spots.append((h, i, (t[j // page], h, j % page, 3 * h % dim)))
+    for _, _, s in spots:
+        c.pool.v[s] = 0
+    y, tol = c.reference()
+    for _, _, s in spots:
+        c.pool.v[s] = 0x7F80
+    c.reload()
+    got = vals(c.run())
+    for h, i, s in spots:
+        sees = i - prefix <= np.arange(n) + own - n
+        assert (got[sees, h, s[3]] == np.inf).all(), (h, i)
+        y[sees, h, s[3]] = got[sees, h, s[3]] = 0.0
+    assert (np.abs(got - y) <= tol).all()
