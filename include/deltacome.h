@@ -709,6 +709,8 @@ typedef struct dc_attn_batch {
  * product as bf16 (as two bf16 pieces where at most 16 rows share the keys),
  * and the row's sum is taken of the weights as they entered; joined in a fixed
  * order, so repeated calls give the same bits; one rounding at the end.
+ * A weight in a sum is 2^12 at most, not 1: finite values of 2^115 / n or more,
+ * where a row sees n keys, may give an infinite result.
  * Contract violations never reach outside the buffers: lengths are cut to the
  * bounds, rows to N, and page numbers outside the cache read page 0; what is
  * written for such sequences is unspecified.

@@ -844,3 +844,16 @@ def test_attention_visible_infinities_of_a_prompt(prefix, std):
         assert (got[sees, h, s[3]] == np.inf).all(), (h, i)
         y[sees, h, s[3]] = got[sees, h, s[3]] = 0.0
     assert (np.abs(got - y) <= tol).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gq", [4, 20, 40])
+def test_attention_large_finite_values(gq, dim):
+    """Values up to 2^115 by the number of keys stay finite (a weight is 2^12 at most, so the sums stay below 2^128)."""
+    note("attention, large finite values", gq, dim)
+    c = Case(gq, nq=[1, 2], kv_len=[70, 66], groups=[0], prefix=[], hq=2 * gq, hkv=2, dim=dim, page=16, kv="bf16", std=3.0)
+    v = vals(c.pool.v)
+    v *= 2.0 ** 115 / 70 / np.nanmax(np.abs(v))
+    c.pool.v = bits(v)
+    c.reload()
+    c.check()
