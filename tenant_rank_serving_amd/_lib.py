@@ -671,11 +671,18 @@ def _rows(t, what: str, n: int, cols: int, device: int) -> int:
     return stride if n > 1 else cols
 
 
+_NO_ROWS = 256   # in place of the address of a tensor without rows (there is none): aligned, never read
+
+
+def _at(t) -> int:
+    return t.data_ptr() or _NO_ROWS
+
+
 def _vector(t, what: str, n: int, dtype, device: int) -> int:
     """The address of a contiguous vector of n elements."""
     if t.shape != (n,) or t.dtype != dtype or t.get_device() != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s [%d] on device %d" % (what, dtype, n, device))
-    return t.data_ptr()
+    return _at(t)
 
 
 def dc_kv_append(cache: KvCache, q, k, v, pos, slots, rope: Rope, q_out, stream=None) -> None:
@@ -699,8 +706,8 @@ def dc_kv_append(cache: KvCache, q, k, v, pos, slots, rope: Rope, q_out, stream=
         if cols != hq * cache.dim:
             raise ValueError("q must have whole heads of %d" % cache.dim)
         qs, qos = _rows(q, "q", n, cols, dev), _rows(q_out, "q_out", n, cols, dev)
-        pq, po = q.data_ptr(), q_out.data_ptr()
-    _check(lib().dc_kv_append(cache.ref, pr, pq, qs, k.data_ptr(), ks, v.data_ptr(), vs, pp, ps, po, qos, hq, n,
+        pq, po = _at(q), _at(q_out)
+    _check(lib().dc_kv_append(cache.ref, pr, pq, qs, _at(k), ks, _at(v), vs, pp, ps, po, qos, hq, n,
                               _current(dev, stream)), "dc_kv_append")
 
 
@@ -753,7 +760,7 @@ def dc_attention(cache: KvCache, q, batch: AttnBatch, scale: float, y, ws, strea
     qs, ys = _rows(q, "q", n, cols, dev), _rows(y, "y", n, cols, dev)
     if batch.device != dev or ws.get_device() != dev:
         raise ValueError("the batch, the workspace and the cache must be on one device")
-    _check(lib().dc_attention(cache.ref, batch.ref, q.data_ptr(), qs, hq, scale, y.data_ptr(), ys, n, _dptr(ws, "ws"),
+    _check(lib().dc_attention(cache.ref, batch.ref, _at(q), qs, hq, scale, _at(y), ys, n, _dptr(ws, "ws"),
                               ws.numel() * ws.element_size(), _current(dev, stream)), "dc_attention")
 
 
@@ -791,4 +798,4 @@ def dc_apply_w4(view: W4View, x, y, stream=None) -> None:
     t, dev = x.shape[0], view.device
     if _rows(x, "x", t, view.inn, dev) != view.inn or _rows(y, "y", t, view.out, dev) != view.out:
         raise ValueError("x and y must be contiguous")
-    _check(lib().dc_apply_w4(view.ref, x.data_ptr(), y.data_ptr(), t, _current(dev, stream)), "dc_apply_w4")
+    _check(lib().dc_apply_w4(view.ref, _at(x), _at(y), t, _current(dev, stream)), "dc_apply_w4")

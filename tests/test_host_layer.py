@@ -212,3 +212,30 @@ def test_attention_scales_at_the_ends(L):
 
 def test_append_of_more_heads_than_a_launch_takes(L):
     assert append(L, hq=1 << 21, qs=1 << 28, qos=1 << 28, n=1, q=1 << 40, qo=1 << 42, k=1 << 43, v=1 << 44) == E.DC_ERR_UNSUPPORTED
+
+
+def test_empty_calls_through_the_binding(monkeypatch):
+    """Tensors without rows have no address; a call with them is a no-op, its other arguments are checked all the same."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(_lib, "_current", lambda device, stream: 0)
+    bf16 = dict(dtype=torch.bfloat16)
+    k = torch.zeros(3, 2, 16, 64, **bf16)
+    c = trs.KvCache(k, k.clone())
+    rope = trs.Rope(torch.ones(32, dtype=torch.float64))
+    row = torch.zeros(1, 128, **bf16)
+    none, pos, slots = row[:0], torch.zeros(0, dtype=torch.int32), torch.zeros(0, dtype=torch.int64)
+    for empty in (none, torch.zeros(0, 128, **bf16)):
+        assert empty.data_ptr() == 0
+        trs.dc_kv_append(c, empty, empty, empty, pos, slots, rope, empty)
+        trs.dc_kv_append(c, None, empty, empty, None, slots, None, None)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    for b in (trs.AttnBatch(i32(1), i32(0), i32(1, 4), 1, 64), trs.AttnBatch(i32(3), i32(2), i32(2, 4), 0, 64)):
+        trs.dc_attention(c, none, b, 0.125, none, ws)
+    view = trs.W4View(128, 128, torch.zeros(trs.dc_w4_bytes(128, 128), dtype=torch.uint8))
+    trs.dc_apply_w4(view, none, none)
+    with pytest.raises(trs.DcError):
+        trs.dc_attention(c, none, trs.AttnBatch(i32(3), i32(2), i32(2, 4), 0, 65), 0.125, none, ws)
+    with pytest.raises(ValueError):
+        trs.dc_kv_append(c, none[:, :64], none, none, pos, slots, rope, none)
