@@ -206,7 +206,7 @@ struct Tiles {
     }
     // 16 bytes a lane from base + voff to lds + 16 lane
     static __device__ __forceinline__ void to_lds(const uint8_t* base, int voff, uint32_t lds) {
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
     }
     // the keys of the tile at k into buffer b, and where its values are
     __device__ __forceinline__ void load_k(const Stream& st, int k, int k1, int b) {

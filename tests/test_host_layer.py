@@ -239,3 +239,18 @@ def test_empty_calls_through_the_binding(monkeypatch):
         trs.dc_attention(c, none, trs.AttnBatch(i32(3), i32(2), i32(2, 4), 0, 65), 0.125, none, ws)
     with pytest.raises(ValueError):
         trs.dc_kv_append(c, none[:, :64], none, none, pos, slots, rope, none)
+
+
+def test_assembly_names_the_registers_it_writes():
+    """Inline assembly that writes m0, exec or vcc by name says so, or the compiler may keep something there."""
+    import re
+    src = os.path.join(os.path.dirname(trs.__file__), "csrc")
+    found = 0
+    for name in sorted(os.listdir(src)):
+        text = open(os.path.join(src, name)).read()
+        for m in re.finditer(r"asm volatile\((.*?)\);", text, re.S):
+            for reg in ("m0", "exec", "vcc"):
+                if re.search(r"[a-z_0-9]+ %s," % reg, m.group(1)):
+                    found += 1
+                    assert '"%s"' % reg in m.group(1).rsplit(":", 1)[1], (name, m.group(1))
+    assert found
