@@ -634,9 +634,10 @@ typedef struct dc_rope {
  *   q         device bf16 [N][q_heads * dim], rows q_stride elements apart; the
  *             same for k and v ([N][kv heads * dim]) and q_out: columns of one
  *             fused projection are such rows.  q_heads = 0: no queries (q and
- *             q_out are not used)
- *   q_out     may be q itself (same pointer and stride); must not overlap k, v
- *             or otherwise q.  Strides: multiples of 8 elements
+ *             q_out are not used).  Rows that lie in the cache must not be
+ *             among the slots that the call stores
+ *   q_out     may be q itself (same pointer and stride); must not overlap k, v,
+ *             the cache or otherwise q.  Strides: multiples of 8 elements
  *   pos       device int32 [N], any position
  *   slots     device int64 [N]: page * tokens per page + slot; a token whose
  *             slot is negative or past the cache is not stored (a padded row:
@@ -695,11 +696,11 @@ typedef struct dc_attn_batch {
  * sees; query head h reads kv head h / (q_heads / kv heads).  A shared prefix
  * is read once for its group's rows.
  *   q, y      device bf16 [N][q_heads * dim], rows q_stride / y_stride apart
- *             (multiples of 8 elements); must not overlap.  Rows behind the
+ *             (multiples of 8 elements); must not overlap, nor y the cache.  Rows behind the
  *             last sequence, and in front of the first, are left as they are
  *   scale     > 0, no subnormal, and finite times log2(e)
  *   ws        ws_bytes >= dc_attention_workspace_bytes(kv, b, q_heads, N), 256-byte
- *             aligned; holds nothing between calls, so calls that follow each
+ *             aligned, apart from q, y and the cache; holds nothing between calls, so calls that follow each
  *             other may share one, and calls that may run at once may not
  * A row that sees no key gets zeros.  What lies in slots that a row does not
  * see (infinities and NaN included) does not reach it; an infinite value that
@@ -748,7 +749,7 @@ size_t dc_w4_bytes(int32_t out, int32_t in);
  * dc_w4_pack_device -- quantize a bf16 matrix [out][in] into the 4-bit format
  * on the GPU (the quantizer of dc_pack at 4 bits).  flag: device uint32, set
  * to 0 by the call and to 1 if an entry is not finite or a scale overflows
- * fp16 (those groups are unspecified).  Errors: DC_ERR_INVALID_ARG,
+ * fp16 (those groups are unspecified).  W and dst must not overlap.  Errors: DC_ERR_INVALID_ARG,
  * DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_BUFFER, DC_ERR_UNSUPPORTED (2^31 entries).
  */
 dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* dst, size_t dst_bytes, uint32_t* flag,
@@ -757,7 +758,7 @@ dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* ds
 /*
  * dc_apply_w4 -- y = W x for T tokens (meant for few; any number is served).
  *   x  device bf16 [T][in], y  device bf16 [T][out], fully overwritten, rounded
- *      once from fp32 sums in a fixed order; must not overlap
+ *      once from fp32 sums in a fixed order; must not overlap, nor y the matrix
  * The codes are multiplied as 128 + q and the 128 + z taken off the group's sum
  * (relative to the group's sum of |x| this costs 2^-17); a token with
  * an entry that is not finite, or of 2^119 or more, may get NaN throughout.

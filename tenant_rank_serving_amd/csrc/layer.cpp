@@ -27,6 +27,30 @@ bool rows_meet(const void* a, int64_t sa, int64_t wa, const void* b, int64_t sb,
   return d < u || d + v > sa;
 }
 
+// The bytes from the first row's first to the last row's last.
+int64_t rows_span(int64_t stride, int64_t w, int64_t n) { return (n - 1) * stride + w; }
+
+bool spans_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// Whether n bytes at p reach into the cache's keys or values (into a page, not
+// into room between pages).
+bool in_cache(const dc::KvArgs& k, int64_t dim_bytes, const void* p, int64_t n) {
+  const int64_t page =
+      (k.heads - 1) * k.head_stride + ((INT64_C(1) << k.shift) - 1) * k.slot_stride + dim_bytes;
+  const int64_t all = (k.num_pages - 1) * k.page_stride + page;
+  for (const uint8_t* base : {k.k, k.v}) {
+    if (!spans_meet(base, all, p, n)) continue;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(base);
+    if (x < b || k.num_pages == 1) return true;
+    const int64_t at = (int64_t)((x - b) % (uintptr_t)k.page_stride);
+    if (at < page || at + n > k.page_stride) return true;
+  }
+  return false;
+}
+
 bool mul_fits(int64_t a, int64_t b, int64_t lim) { return a == 0 || b <= lim / a; }
 
 // A launch's threads along x are numbered with 32 bits; blocks of 256.
@@ -196,6 +220,8 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
   if (!aligned(slots, 8)) return DC_ERR_ALIGN;
   if (N > kMostBlocks) return DC_ERR_UNSUPPORTED;   // a block a token
   if (N == 0) return DC_OK;
+  const int64_t row = (int64_t)kv->dim * (kv->dtype == DC_KV_BF16 ? 2 : 1);
+  if (q_heads > 0 && in_cache(a.kv, row, q_out, rows_span(2 * q_out_stride, 2 * qc, N))) return DC_ERR_INVALID_ARG;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -256,6 +282,11 @@ dc_status dc_attention(const dc_kv_cache* kv, const dc_attn_batch* b, const uint
   if (blocks_of(a.plan, b->seqs, b->groups, kv->heads) > kMostBlocks) return DC_ERR_UNSUPPORTED;
   if (!a.plan.direct && ((int64_t)N * q_heads + 3) / 4 > kMostBlocks) return DC_ERR_UNSUPPORTED;   // the join
   if (N == 0 || b->seqs == 0 || b->max_q == 0) return DC_OK;   // no query: nothing to write
+  const int64_t row = (int64_t)kv->dim * (kv->dtype == DC_KV_BF16 ? 2 : 1), need = (int64_t)a.plan.ws;
+  const int64_t y_span = rows_span(2 * y_stride, 2 * qc, N), q_span = rows_span(2 * q_stride, 2 * qc, N);
+  if (in_cache(a.kv, row, y, y_span) || spans_meet(ws, need, y, y_span) || spans_meet(ws, need, q, q_span) ||
+      (need > 0 && in_cache(a.kv, row, ws, need)))
+    return DC_ERR_INVALID_ARG;
   a.q = q;
   a.y = y;
   a.qs = q_stride;
@@ -309,6 +340,7 @@ dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* ds
   if (!aligned(W, 16) || !aligned(dst, 16) || !aligned(flag, 4)) return DC_ERR_ALIGN;
   if (dst_bytes < need) return DC_ERR_BUFFER;
   if ((size_t)out * in > (size_t)INT32_MAX) return DC_ERR_UNSUPPORTED;
+  if (spans_meet(W, 2 * (int64_t)out * in, dst, (int64_t)need)) return DC_ERR_INVALID_ARG;
   return dc::launch_w4_pack(out, in, W, static_cast<uint8_t*>(dst), flag, stream) == 0 ? DC_OK : DC_ERR_HIP;
 }
 
@@ -321,6 +353,7 @@ dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32
     return DC_ERR_INVALID_ARG;
   if ((size_t)w->out * w->in > (size_t)INT32_MAX || T > 65535 * 16) return DC_ERR_UNSUPPORTED;
   if (T == 0) return DC_OK;
+  if (spans_meet(w->base, (int64_t)dc_w4_bytes(w->out, w->in), y, 2 * (int64_t)w->out * T)) return DC_ERR_INVALID_ARG;
   const dc::W4Args a{static_cast<const uint8_t*>(w->base), x, y, w->out, w->in, T, stream};
   return dc::launch_w4(a) == 0 ? DC_OK : DC_ERR_HIP;
 }

@@ -254,3 +254,39 @@ def test_assembly_names_the_registers_it_writes():
                     found += 1
                     assert '"%s"' % reg in m.group(1).rsplit(":", 1)[1], (name, m.group(1))
     assert found
+
+
+# The made-up cache: keys 0x10000 .. 0x38000, values 0x4000000 .. 0x4028000, pages of 0x4000 bytes.
+@pytest.mark.parametrize("kw", [
+    dict(qo=0x10000), dict(qo=0x38000 - 16), dict(qo=0x4000000), dict(qo=0x10000 - 2048, n=2), dict(qo=0x4020000, qos=1 << 12),
+    dict(q=0x20000, qs=1024, qo=0x20000),   # in place, in the cache
+])
+def test_append_refuses_queries_in_the_cache(L, kw):
+    assert append(L, **dict(dict(n=1), **kw)) == E.DC_ERR_INVALID_ARG
+
+
+def test_append_queries_in_a_gap_of_the_cache(L):
+    """Pages with room between them: what fits there is not in the cache (of two tokens, it reaches the next page)."""
+    gap = cache(page_stride=2 * 4 * 16 * 128)   # 0x8000 bytes, the upper half is free
+    assert append(L, gap, n=3, qo=0x10000 + 0x4000 + 0x3000 + 2048) == E.DC_ERR_INVALID_ARG
+    assert append(L, gap, n=1, qo=0x10000 + 0x4000 - 16) == E.DC_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=0x10000), dict(y=0x4028000 - 16), dict(y=0x4000000 - 2048),        # the output in the cache
+    dict(ws=0x10000), dict(ws=0x4020000), dict(ws=0x10000 - 0x2000),          # the workspace in the cache,
+    dict(ws=0x8000000), dict(ws=0x8000000 - 0x2000),                          # in the queries,
+    dict(ws=0x8300000), dict(y=0x101000, ws=0x100000),                        # in the output
+])
+def test_attention_refuses_overlaps(L, kw):
+    assert 0x2000 < L.dc_attention_workspace_bytes(ctypes.byref(cache()), ctypes.byref(batch()), 8, 2) < 0x10000
+    assert attend(L, **dict(dict(n=2, ws=0x100000, nws=0x10000), **kw)) == E.DC_ERR_INVALID_ARG
+
+
+def test_w4_refuses_overlaps(L):
+    size = trs.dc_w4_bytes(256, 384)
+    assert w4(L, t=1, y=0x1000000) == E.DC_ERR_INVALID_ARG and w4(L, t=1, y=0x1000000 + size - 16) == E.DC_ERR_INVALID_ARG
+    pack = lambda w, d: L.dc_w4_pack_device(256, 384, w, d, 1 << 30, 0x100, None)  # noqa: E731
+    assert pack(0x1000000, 0x1000000) == E.DC_ERR_INVALID_ARG
+    assert pack(0x1000000, 0x1000000 + 2 * 256 * 384 - 16) == E.DC_ERR_INVALID_ARG
+    assert pack(0x1000000, 0x1000000 - size + 16) == E.DC_ERR_INVALID_ARG
