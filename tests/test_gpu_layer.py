@@ -2,6 +2,8 @@
 attention over shared prefixes, products with a 4-bit backbone, and a layer's step that runs them together.
 
 Every unused slot of a cache holds NaN, so that anything read from where it must not be shows."""
+import os
+
 import numpy as np
 import pytest
 
@@ -857,3 +859,31 @@ def test_attention_large_finite_values(gq, dim):
     c.pool.v = bits(v)
     c.reload()
     c.check()
+
+
+# The tile that the launcher takes (16-row tiles of the matrix x 16-token tiles of a block), tokens, rows, inputs: each tile,
+# with rows that fill the last block in part (of 3 and 6 row tiles; rows come by 8) and tokens that do.
+W4_TILES = [((1, 1), 5, 640, 1152), ((2, 1), 3, 4224, 256), ((3, 1), 7, 8320, 256), ((3, 1), 16, 11008, 128), ((4, 1), 9, 12416, 256),
+            ((4, 1), 64, 4096, 256), ((6, 1), 2, 16640, 256), ((8, 1), 33, 8320, 256), ((2, 2), 17, 4224, 1152), ((4, 2), 19, 8448, 256),
+            ((6, 2), 17, 16640, 256), ((6, 2), 64, 11008, 128), ((8, 2), 45, 12416, 256), ((8, 2), 33, 12544, 1152)]
+
+
+def w4_tile(tokens, out):
+    """The launcher's rule once more."""
+    def cost(tile):
+        rt, tok = tile[0], 16 * tile[1]
+        blocks = -(-out // 16 // rt) * -(-tokens // tok)
+        return (blocks + 255) // 256 * (17 * rt + 4 * min(tokens, tok))
+    return min([(1, 1), (2, 1), (3, 1), (4, 1), (6, 1), (8, 1), (2, 2), (4, 2), (6, 2), (8, 2)], key=cost)
+
+
+@pytest.mark.parametrize("tile,t_,out,inn", W4_TILES)
+def test_w4_every_tile(tile, t_, out, inn):
+    src = open(os.path.join(os.path.dirname(trs.__file__), "csrc", "k_w4.hip")).read()
+    assert "const int64_t cost = (blocks + 255) / 256 * (17 * rt + 4 * (a.T < tok ? a.T : tok));" in src, "another rule: other cases"
+    assert w4_tile(t_, out) == tile
+    test_w4(t_, out, inn)
+
+
+def test_w4_tiles_are_all_there():
+    assert len({c[0] for c in W4_TILES}) == 10
