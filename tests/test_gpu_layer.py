@@ -887,3 +887,29 @@ def test_w4_every_tile(tile, t_, out, inn):
 
 def test_w4_tiles_are_all_there():
     assert len({c[0] for c in W4_TILES}) == 10
+
+
+# Paths that only long keys or other numbers of heads take.  A range of keys is at most 1/64 of them and holds 128 or more;
+# a wave keeps 64 page numbers at a time, 1024 keys of pages of 16.
+PATHS = {
+    # more than 64 partial sums of a row, and the most there are, 64 of the prefix and 64 of the own keys
+    "72 ranges": dict(nq=[1], kv_len=[9000], groups=[0, 1], prefix=[9000], hq=8, hkv=4, page=16),
+    "128 ranges": dict(nq=[1], kv_len=[8192], groups=[0, 1], prefix=[16384], hq=8, hkv=4, page=16),
+    # between 17 and 64 of them, some of them without keys
+    "20 ranges": dict(nq=[2, 1], kv_len=[1500, 300], groups=[0, 2], prefix=[1900], hq=6, hkv=6, page=64),
+    # long queries: a block of 128 rows walks 69 pages
+    "a prompt on 69 pages": dict(nq=[40], kv_len=[1100], groups=[0], prefix=[], hq=140, hkv=140, page=16),
+    "a prompt on a prefix of 67 pages": dict(nq=[40], kv_len=[50], groups=[0, 1], prefix=[1060], hq=140, hkv=140, page=16),
+    # one range of 69 pages, by 1 and by 20 rows a kv head; of a prefix too
+    "a token on 69 pages": dict(nq=[1, 1], kv_len=[1100, 1030], groups=[0], prefix=[], hq=128, hkv=128, page=16),
+    "20 heads on 69 pages": dict(nq=[1, 1], kv_len=[1100, 1030], groups=[0], prefix=[], hq=2560, hkv=128, page=16),
+    "tokens on 4 prefixes of 69 pages": dict(nq=[1] * 5, kv_len=[3, 90, 1, 0, 17], groups=[0, 1, 2, 3, 5],
+                                             prefix=[1100, 1040, 30, 1090], hq=128, hkv=128, page=16),
+}
+
+
+@pytest.mark.parametrize("name,dim,kv", [(name, dim, kv) for name in PATHS for dim in (64, 128) for kv in ("bf16", "e4m3")
+                                         if "ranges" in name or (dim == 128) == (kv == "bf16")])
+def test_attention_long_paths(name, dim, kv):
+    note("attention, long paths", name, dim, kv)
+    Case(len(name), dim=dim, kv=kv, **PATHS[name]).check()
