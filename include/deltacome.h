@@ -760,8 +760,9 @@ dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* ds
  *   x  device bf16 [T][in], y  device bf16 [T][out], fully overwritten, rounded
  *      once from fp32 sums in a fixed order; must not overlap, nor y the matrix
  * The codes are multiplied as 128 + q and the 128 + z taken off the group's sum
- * (relative to the group's sum of |x| this costs 2^-17); a token with
- * an entry that is not finite, or of 2^119 or more, may get NaN throughout.
+ * (relative to the group's sum of |x| this costs 2^-17); a token with an entry
+ * that is not finite, or with a group whose |x| sum to 2^120 or more (as 128
+ * entries of 2^113 do), may get NaN throughout.
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
  * (2^31 entries, or more than 1048560 tokens).
  */

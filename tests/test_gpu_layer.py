@@ -913,3 +913,21 @@ PATHS = {
 def test_attention_long_paths(name, dim, kv):
     note("attention, long paths", name, dim, kv)
     Case(len(name), dim=dim, kv=kv, **PATHS[name]).check()
+
+
+@pytest.mark.parametrize("t_", [1, 40])
+def test_w4_large_entries(t_):
+    """A group whose entries sum to less than 2^120 (143 of them, the largest code, stay below 2^128); beside it a token
+    with entries that may overflow spoils its own row only."""
+    t = torch()
+    note("w4, large entries", t_)
+    rng = np.random.default_rng(t_)
+    out, inn = 256, 384
+    codes, scale, zero, view = w4_case(rng, out, inn)
+    x = vals(bits(rng.uniform(0.5, 0.99, size=(t_ + 1, inn)) * 2.0 ** 113 * np.where(rng.random((t_ + 1, 1)) < 0.5, 1, rng.choice([-1, 1], (t_ + 1, inn)))))
+    assert np.abs(x).reshape(t_ + 1, -1, 128).sum(-1).max() < 2.0 ** 120
+    x[t_] *= 2.0 ** 5
+    y = t.empty((t_ + 1, out), dtype=t.bfloat16, device="cuda")
+    trs.dc_apply_w4(view, dev_bf16(x), y)
+    want, tol = w4_reference(codes, scale, zero, x)
+    assert (np.abs(vals(host_bits(y)) - want) <= tol)[:t_].all()
