@@ -648,7 +648,7 @@ typedef struct dc_rope {
  * (infinities too; NaN stays NaN).
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
  * (a page's slots of one head span 1 GiB or more, 2^24 tokens or more, more
- * than 2^27 elements of q, k and v a token).
+ * than 65535 * 4096 elements of q, k and v a token).
  * N = 0 is a no-op (of valid arguments: the pointers are not NULL).
  */
 dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_t* q, int64_t q_stride,

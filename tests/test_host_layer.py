@@ -290,3 +290,11 @@ def test_w4_refuses_overlaps(L):
     assert pack(0x1000000, 0x1000000) == E.DC_ERR_INVALID_ARG
     assert pack(0x1000000, 0x1000000 + 2 * 256 * 384 - 16) == E.DC_ERR_INVALID_ARG
     assert pack(0x1000000, 0x1000000 - size + 16) == E.DC_ERR_INVALID_ARG
+
+
+def test_append_elements_of_a_token_at_the_limit(L):
+    """65535 * 4096 elements of q, k and v a token, 16 a unit and 256 units a block along the launch's y."""
+    most = 65535 * 4096 // 128 - 2 * 4          # query heads beside 4 + 4 kv heads
+    far = dict(q=1 << 40, qs=1 << 29, qo=1 << 42, qos=1 << 29, k=1 << 43, v=1 << 44)
+    assert append(L, hq=most, **far) == E.DC_OK
+    assert append(L, hq=most + 1, **far) == E.DC_ERR_UNSUPPORTED
