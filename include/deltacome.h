@@ -678,7 +678,15 @@ dc_status dc_kv_append(const dc_kv_cache* kv, const dc_rope* rope, const uint16_
  * The bounds choose one form for the whole call: with long queries (more than
  * 32 rows of a kv head, in 64 blocks of 128 or more) a sequence's keys are read
  * by the blocks of its rows alone, so single tokens with many keys are better
- * off in a call of their own, beside the one for the prompts.
+ * off in a call of their own, beside the one for the prompts.  In that form a
+ * prefix is read once for every block of 128 rows; where such blocks would walk
+ * 1.9 times the keys that blocks filled from a whole group do, and with fewer
+ * rows always, it is read once for its group's rows.
+ * Without long queries a sequence's keys are cut into ranges by max_kv, seqs and
+ * the kv heads alone.  The work is even when max_kv is close to the lengths; one
+ * long sequence among many short ones, or a bound far above every length,
+ * leaves its ranges to few blocks: call with such sequences by themselves, and
+ * with a bound near what the batch holds.
  */
 typedef struct dc_attn_batch {
   int32_t seqs, max_q, max_kv, seq_pages;
@@ -693,8 +701,7 @@ typedef struct dc_attn_batch {
 
 /*
  * dc_attention -- y = sum_k softmax_k(scale q.k) v_k over the keys each query
- * sees; query head h reads kv head h / (q_heads / kv heads).  A shared prefix
- * is read once for its group's rows.
+ * sees; query head h reads kv head h / (q_heads / kv heads).
  *   q, y      device bf16 [N][q_heads * dim], rows q_stride / y_stride apart
  *             (multiples of 8 elements); must not overlap, nor y the cache.  Rows behind the
  *             last sequence, and in front of the first, are left as they are

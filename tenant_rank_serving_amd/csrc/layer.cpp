@@ -137,7 +137,18 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   // 4096 keys 108 / 110; 512 x 8192 263 / 274; 128 x 512 18.7 / 26.6, x 1024
   // 31.6 / 33.5, x 2048 56 / 47; 64 x 512 18.3 / 21.1, x 1024 31 / 25)
   const int64_t rb = (ro + 127) / 128, all = (int64_t)B * hkv * rb;
-  if (ro > 32 && (all >= 256 || (all >= 64 && (int64_t)max_kv + (G > 0 ? max_pre : 0) <= 8 * all))) {
+  // Each of those blocks walks its sequence's prefix too; split, the blocks of a
+  // prefix are filled from all rows of its group, at the price of partial sums.
+  // Keys walked by blocks, in rows / split (us, in rows / split; 36 rows of a
+  // sequence and kv head, 8 kv heads, 300 own keys): 64 sequences on one prefix
+  // of 16384 3.4 (433 / 208), of 2048 2.7 (78 / 60), of 512 1.8 (38 / 47); on 8
+  // of 16384 2.6 (436 / 287), of 2048 2.2 (75 / 70), of 512 1.7 (36 / 48); 64
+  // rows, one prefix of 16384 2.0 (434 / 310), of 2048 1.8 (76 / 76); 128 rows
+  // (filled blocks) of 16384 1.0 (526 / 567).
+  const int64_t keys = (int64_t)max_kv + (G > 0 ? max_pre : 0);
+  const double in_rows = (double)B * rb * keys, in_split = (double)G * ((rg + 127) / 128) * max_pre + (double)B * rb * max_kv;
+  const bool shared = G > 0 && in_rows >= 1.9 * in_split;
+  if (ro > 32 && !shared && (all >= 256 || (all >= 64 && keys <= 8 * all))) {
     p.rows = true;
     p.rbo = (int32_t)rb;
     p.co = p.cp = 128;

@@ -900,6 +900,11 @@ PATHS = {
     # long queries: a block of 128 rows walks 69 pages
     "a prompt on 69 pages": dict(nq=[40], kv_len=[1100], groups=[0], prefix=[], hq=140, hkv=140, page=16),
     "a prompt on a prefix of 67 pages": dict(nq=[40], kv_len=[50], groups=[0, 1], prefix=[1060], hq=140, hkv=140, page=16),
+    # 36 rows of a sequence, 5 blocks of 128 from the 16 of its group (ranges of the prefix); from 3 groups
+    "drafted tokens on one prefix, ranges": dict(nq=[9] * 16, kv_len=[20 + i for i in range(16)], groups=[0, 16], prefix=[700], hq=32,
+                                                 hkv=8, page=16),
+    "drafted tokens on 3 prefixes, ranges": dict(nq=[9] * 15 + [0], kv_len=[9 + i for i in range(16)], groups=[0, 7, 8, 16],
+                                                 prefix=[500, 900, 411], hq=64, hkv=16, page=32),
     # one range of 69 pages, by 1 and by 20 rows a kv head; of a prefix too
     "a token on 69 pages": dict(nq=[1, 1], kv_len=[1100, 1030], groups=[0], prefix=[], hq=128, hkv=128, page=16),
     "20 heads on 69 pages": dict(nq=[1, 1], kv_len=[1100, 1030], groups=[0], prefix=[], hq=2560, hkv=128, page=16),

@@ -298,3 +298,15 @@ def test_append_elements_of_a_token_at_the_limit(L):
     far = dict(q=1 << 40, qs=1 << 29, qo=1 << 42, qos=1 << 29, k=1 << 43, v=1 << 44)
     assert append(L, hq=most, **far) == E.DC_OK
     assert append(L, hq=most + 1, **far) == E.DC_ERR_UNSUPPORTED
+
+
+def test_attention_reads_a_shared_prefix_for_its_group(L):
+    """9 drafted tokens of 64 sequences on one long prefix: 36 rows of 128 in a block of their own, so the blocks of the
+    prefix are filled from the group (with partial sums); filled blocks walk it themselves."""
+    c = cache(heads=8, page_stride=8 * 16 * 128, num_pages=20000)
+    def size(seqs, nq, own, groups, prefix):
+        b = batch(seqs=seqs, max_q=nq, max_kv=own, seq_pages=1 << 12, groups=groups, max_group_q=seqs // groups * nq, max_prefix=prefix,
+                  prefix_pages_per_group=1 << 12)
+        return L.dc_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 32, seqs * nq)
+    assert size(64, 9, 300, 1, 16384) > 256 and size(64, 9, 300, 8, 16384) > 256 and size(64, 9, 300, 1, 2048) > 256
+    assert size(64, 9, 300, 1, 512) == 256 and size(64, 32, 300, 1, 16384) == 256 and size(8, 1024, 1024, 8, 2048) == 256
