@@ -147,7 +147,7 @@ AttnPlan attn_plan(int32_t hkv, int32_t gq, int32_t dim, int32_t n, int32_t B, i
   // (filled blocks) of 16384 1.0 (526 / 567).
   const int64_t keys = (int64_t)max_kv + (G > 0 ? max_pre : 0);
   const double in_rows = (double)B * rb * keys, in_split = (double)G * ((rg + 127) / 128) * max_pre + (double)B * rb * max_kv;
-  const bool shared = G > 0 && in_rows >= 1.9 * in_split;
+  const bool shared = G > 0 && in_rows >= 1.9 * in_split && ((int64_t)n * hkv * gq + 3) / 4 <= kMostBlocks;   // (a join of theirs)
   if (ro > 32 && !shared && (all >= 256 || (all >= 64 && keys <= 8 * all))) {
     p.rows = true;
     p.rbo = (int32_t)rb;

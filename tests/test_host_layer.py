@@ -309,4 +309,5 @@ def test_attention_reads_a_shared_prefix_for_its_group(L):
                   prefix_pages_per_group=1 << 12)
         return L.dc_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 32, seqs * nq)
     assert size(64, 9, 300, 1, 16384) > 256 and size(64, 9, 300, 8, 16384) > 256 and size(64, 9, 300, 1, 2048) > 256
+    assert size(400000, 9, 16, 100, 16384) == 256   # more rows than a join takes: not refused
     assert size(64, 9, 300, 1, 512) == 256 and size(64, 32, 300, 1, 16384) == 256 and size(8, 1024, 1024, 8, 2048) == 256
