@@ -1,6 +1,7 @@
 // The walk for more than 32 query rows: a block takes 128 rows, wave w rows
-// 32w .. 32w+31, and its keys come through LDS in tiles that all waves share.  Included inside namespace dc, anonymous namespace, of k_attn.hip,
-// behind attn_common.h.
+// 32w .. 32w+31, and its keys come through LDS in tiles that all waves share.
+// Included inside namespace dc, anonymous namespace, of k_attn.hip, behind
+// attn_common.h.
 //
 // Products transposed as for few rows, S^T = K Q^T and O^T = V^T P^T, here
 // 32x32x16: a wave reads a tile's keys and values once for 32 rows.
@@ -17,13 +18,15 @@
 //       value_swizzle).  bf16 keys go straight to LDS (global_load_lds, no
 //       registers; the lanes choose the permuted pieces); e4m3 codes pass
 //       through registers and are converted, once a block.
-// Measured, 8 prompts of up to 2048 tokens, 32 heads on 8, bf16: 181 us, 845
-// TFLOP/s.  In the middle of a block the matrix cores are busy 68 % of the
-// time, as in a large library product, at a clock that the power limit sets
-// (1.83 GHz; with two blocks a CU 58 % at 1.93, the same time); the rest is a
-// block's first loads and its output (14000 of 60000 cycles) and the last
-// blocks.  Without any exponentials it would take 160 us, without reading LDS
-// 173.
+// Weights enter as one bf16 piece, rounded like the output (2^-8), and their sum
+// is taken as they entered; a second piece would cost half of the products again
+// (8 prompts 185 -> 242 us, 48 chats on an e4m3 prefix 52.7 -> 61.8).
+// Measured, 8 prompts of up to 2048 tokens, 32 heads on 8, bf16: 181 to 191 us
+// from one card to another, 840 to 800 TFLOP/s; with e4m3 keys 212 where bf16
+// takes 191.  The matrix cores are busy 41 % of the call, at 1.84 GHz: 68 % inside
+// the loop, less a block's first loads and its output (14000 of its 60000 cycles)
+// and the last blocks (25 us).  Without any exponentials it would take 9 us
+// less, without reading LDS 12.
 #pragma once
 
 __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
@@ -299,7 +302,7 @@ struct Tiles {
   // the keys of the one behind that set out, into the places that the step
   // before freed: each is on its way for two steps, with one barrier a step.
   // Three tiles of 32 keys take 48 KB (D = 128), so three blocks share a CU
-  // (three waves a SIMD at 160 registers).
+  // (three waves a SIMD at 168 registers).
   template <int B>
   __device__ __forceinline__ void one_step(Stage& g, const Stream& st, f32x16& s, int k, int k1, int lo, int up, int blo,
                                            int bup, float c, const int* ko, const int* vo, Lds& sh) {

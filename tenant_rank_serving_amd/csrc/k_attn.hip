@@ -11,10 +11,11 @@
 //   rows    long queries: a block takes 128 rows of one (sequence, kv head)
 //           and walks its prefix and its own keys; no partial sums.
 // Measured (own keys and prefix are read once, us): one token on 1000 keys of
-// 32 heads 7.5 + 3.0 for the join, latency; 64 tokens in 16 groups on prefixes
-// of 2048 51 + 5, 4.3 TB/s; 48 tokens on one e4m3 prefix of 30000 keys 47 + 7,
-// the matrix products of 192 rows in blocks of 128; 20 x 5 tokens of 40 heads on
-// 3 prefixes of 1111 40 + 6.
+// 32 heads 7.7 + 3.0 for the join, latency; 64 tokens in 16 groups on prefixes
+// of 2048 51 + 5, 4.3 TB/s, in two rounds of blocks; 48 tokens on one e4m3 prefix
+// of 30000 keys 48 + 7, 192 rows in blocks of 128, 864 blocks of which 512 run at
+// once; 20 x 5 tokens of 40 heads on 3 prefixes of 1111 41 + 6, 1160 blocks of
+// which 768 run at once.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

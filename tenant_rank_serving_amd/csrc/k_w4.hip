@@ -184,16 +184,21 @@ void go(const W4Args& a) {
 
 }  // namespace
 
-// The tile of a block.  A CU reads about 17 bytes a nanosecond through its L1
-// when all read (x comes from L2 again in every block), so the time is that
-// of what the fullest CU reads: RT row tiles of the matrix (8.5 bytes an
-// input with the scales) and the tokens' x (2 bytes an input each), for each
-// round of 256 blocks.  Measured, us, all 10 tiles timed: 4096 x 4096 with 64
-// tokens (1,1) 18.6, (1,4) 17.1, (4,1) 8.8; 11008 x 4096 with 16 (1,1) 14.7,
-// (2,1) 11.6, (3,1) 8.2, (4,1) 9.0, with 64 (4,4) 21.5, (3,4) 20.3, (6,2)
-// 15.1; 4096 x 14336 with 1 (1,1) 10.3, (2,1) 12.6.  4096 x 14336 with 7 tokens
-// takes 10.6 however many groups are loaded ahead (2 to 8), with 8 waves or 16,
-// and wherever a block begins in x.
+// The tile of a block.  With more than a token or two the time is that of a
+// CU's L1, about an access a cycle.  A wave's load makes 16 accesses where its
+// bytes lie together (codes; x of one token, whose row all lanes read), and
+// more where they are 16 rows of x: counted 16 a load with 1 token, 29 with 7,
+// 36 in the tile (6,2) with 64, whose 23000 accesses a CU take two thirds of the
+// time.  Each block loads x again for its rows, so the rule weighs, for the
+// fullest CU, RT row tiles (17 each) against the tokens' x (4 each), for each
+// round of 256 blocks; of 4096 inputs 14 to 17 such units take a us.  Measured,
+// us, all 10 tiles timed: 4096 x 4096 with 64 tokens (1,1) 18.6, (1,4) 17.1,
+// (4,1) 8.8; 11008 x 4096 with 16 (1,1) 14.7, (2,1) 11.6, (3,1) 8.2, (4,1) 9.0,
+// with 64 (4,4) 21.5, (3,4) 20.3, (6,2) 15.1; 4096 x 14336 with 1 (1,1) 10.3 (3.0
+// TB/s: few bytes on their way), (2,1) 12.6.  4096 x 14336 with 7 tokens takes
+// 10.6 however many groups are loaded ahead (2 to 8), with 8 waves or 16, and
+// wherever a block begins in x.  4096 x 4096 with 128, 512 and 2048 tokens 13, 36
+// and 128: every 32 tokens unpack the codes again.
 int launch_w4(const W4Args& a) {
   constexpr int kTiles[][2] = {{1, 1}, {2, 1}, {3, 1}, {4, 1}, {6, 1}, {8, 1}, {2, 2}, {4, 2}, {6, 2}, {8, 2}};
   int best = 0;
