@@ -775,6 +775,213 @@ dc_status dc_w4_pack_device(int32_t out, int32_t in, const uint16_t* W, void* ds
  */
 dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32_t T, void* stream);
 
+/*
+ * What closes a decode step: verifying drafted tokens, the page tables and
+ * pages of a cache, and a backbone in microscaled 4-bit floating point.
+ * Conventions as for every call.
+ *
+ * dc_verify_drafts -- which drafted tokens stand, and the token after them.
+ * Row r of `target` holds the model's logits behind input token r of a step;
+ * sequence b's rows are q_start[b] .. q_start[b+1]-1, and its input tokens
+ * after the first are its drafts (a row more than drafts; no drafts: plain
+ * sampling; no rows: nothing).  Row r's draft is thus tokens[r+1].  With
+ *     p = softmax(target[r] / T),   q = softmax(draft[r] / T),
+ * T the sequence's temperature, drafts are looked at in order, and d stands if
+ *     accept[r] q(d) < p(d).
+ * At the first one that does not, the new token is drawn from max(p - q, 0)
+ * (from p where that is zero everywhere), behind the last one from p: the
+ * lowest i with sum_{k<=i} w_k > pick[b] sum_k w_k and w_i > 0.
+ *   draft        NULL: q is 1 at the drafted token (drafts that were looked up,
+ *                or the draft model's likeliest)
+ *   temperature  NULL: 1.  Not above zero (or NaN): greedy, a draft stands if it
+ *                is the lowest token of the largest logit, which is the new one
+ *                otherwise; accept, pick and draft are not used
+ *   out, prob    [N]: in a sequence's rows the drafts that stood, the new token,
+ *                then -1; p of each (greedy: 1), then 0.  prob may be NULL
+ *   count        [seqs]: how many tokens that is, the new one among them
+ * Rows behind the last sequence, and in front of the first, are left as they
+ * are.  Logits of -inf are tokens that cannot be drawn.  A row of p without a
+ * distribution (a NaN or +inf, or -inf throughout) ends its sequence: no draft
+ * stands there and there is no new token (-1, not counted).  A draft whose
+ * token is outside the vocabulary, or whose row of q has no distribution, does
+ * not stand; the new token is then drawn from p (of q with a token outside the
+ * vocabulary: from max(p - q, 0)).
+ *   target, draft  device [N][vocab] of `dtype`, rows `stride` elements apart
+ *                (>= vocab; any alignment of whole elements).  draft's row of a
+ *                sequence's last row is not read
+ *   ws           ws_bytes >= dc_verify_workspace_bytes(vocab, N, seqs), 256-byte
+ *                aligned; holds nothing between calls
+ * Arithmetic: weights, sums and comparisons in fp64 (the exponentials to 2e-14),
+ * in a fixed order: the tokens are those of the formula wherever its two sides
+ * differ by more than about 1e-13 of the sum.
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_BUFFER,
+ * DC_ERR_UNSUPPORTED (a vocabulary of more than 2^30, 2^24 pieces of 8192
+ * logits or more, or rows that lie
+ * beyond 2^47 bytes).
+ */
+enum { DC_LOGITS_BF16 = 0, DC_LOGITS_F32 = 1 };
+
+typedef struct dc_verify_batch {
+  int32_t seqs;
+  const int32_t* q_start;   /* device [seqs+1], non-decreasing */
+  const int32_t* tokens;    /* device [N]: the step's input tokens */
+  const float* accept;      /* device [N], uniform in [0, 1) */
+  const float* pick;        /* device [seqs], uniform in [0, 1) */
+  const float* temperature; /* device [seqs] or NULL */
+} dc_verify_batch;
+
+size_t dc_verify_workspace_bytes(int32_t vocab, int32_t N, int32_t seqs);
+dc_status dc_verify_drafts(const dc_verify_batch* b, int32_t dtype, int32_t vocab, const void* target,
+                           int64_t target_stride, const void* draft, int64_t draft_stride, int32_t N, int32_t* out,
+                           int32_t* count, float* prob, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dc_kv_table -- the page tables of a cache's sequences (the `pages` and
+ * `kv_len` of dc_attn_batch) and how many entries hold each page: all of it
+ * device memory that these calls keep, so that a captured step can follow it.
+ * One table serves all layers of a model (their caches are numbered alike).
+ *   pages   [seqs][width]: sequence b's first ceil(kv_len[b] / page) entries are
+ *           page numbers; entries that a call gives back become -1
+ *   refs    [num_pages], 16-byte aligned: entries that hold the page; 0 (or
+ *           below): free
+ *   status  [1]: bits are or-ed into it, the caller clears it:
+ *           DC_KV_FULL   too few free pages for some sequence
+ *           DC_KV_BAD    a length, row or page number out of range, or a row
+ *                        that a fork would have overwritten; the entry or
+ *                        sequence concerned was left out
+ */
+enum { DC_KV_FULL = 1, DC_KV_BAD = 2 };
+
+typedef struct dc_kv_table {
+  int32_t seqs, width;
+  int32_t page, num_pages;
+  int32_t* pages;
+  int32_t* kv_len;
+  int32_t* refs;
+} dc_kv_table;
+
+/*
+ * dc_kv_resize -- sequences take new lengths: new_len[b] for each.
+ *   1. Pages behind a new length are given back (refs - 1, the entry -1).
+ *   2. Pages that new tokens need are taken: free ones, lowest numbers first,
+ *      for the sequences in order.  A sequence that grows, and whose last page
+ *      is partly filled and held by others too (refs > 1 after 1.), gets a fresh
+ *      one in its place, before its further ones: copies[b] = {that page, the
+ *      fresh one} for dc_kv_copy, {-1, -1} for the other sequences; the old
+ *      page's count falls at the end of the call.
+ *   3. kv_len[b] = new_len[b].
+ * A sequence for which the free pages do not suffice, and those behind it that
+ * need any, stay as they are (DC_KV_FULL); they lose no page to it.  New
+ * pages' slots hold what they held.  new_len may be kv_len itself (nothing
+ * happens then).
+ *   copies  device int32 [seqs][2]
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
+ * (more than DC_KV_MAX_SEQS sequences, tables of 2^30 entries).
+ */
+#define DC_KV_MAX_SEQS 16384
+dc_status dc_kv_resize(const dc_kv_table* t, const int32_t* new_len, int32_t* copies, uint32_t* status, void* stream);
+
+/*
+ * dc_kv_fork -- row dst[i] becomes a branch of row src[i]: the same pages
+ * (refs + 1 each) and length, nothing copied (dc_kv_resize exchanges the last
+ * page when one of them grows).  dst[i] has to be empty (kv_len 0, else
+ * DC_KV_BAD and left out); a row may be src any number of times, dst once, and
+ * not both.
+ *   src, dst  device int32 [n]
+ */
+dc_status dc_kv_fork(const dc_kv_table* t, const int32_t* src, const int32_t* dst, int32_t n, uint32_t* status,
+                     void* stream);
+
+/*
+ * dc_kv_copy -- whole pages of all layers: copies[i] = {from, to}, keys and
+ * values, in one launch.  Pairs with a number outside the cache are left out
+ * (those of dc_kv_resize that need no copy).  A page that is `to` must not be in
+ * any other pair (of two writes either's pieces may be found there).
+ *   layers  host array [n_layers] of caches that differ in k, v (and scales)
+ *           only, 1 .. DC_KV_MAX_LAYERS; no two may overlap
+ *   copies  device int32 [n][2]
+ * Errors as for dc_kv_append's cache; DC_ERR_SHAPE if the caches differ,
+ * DC_ERR_UNSUPPORTED (more layers, or more than 2^24 blocks of 16 KiB).
+ */
+#define DC_KV_MAX_LAYERS 128
+dc_status dc_kv_copy(const dc_kv_cache* layers, int32_t n_layers, const int32_t* copies, int32_t n, void* stream);
+
+/*
+ * dc_kv_compact -- sequences keep some of their tokens: token keep[j] of
+ * sequence b goes to position j - keep_start[b], for keep_start[b] <= j <
+ * keep_start[b+1], in all layers (keys stay turned as they are).  The caller's
+ * next dc_kv_resize gives back what is left behind the kept tokens.
+ *   from      device int32 [seqs][width]: page tables
+ *   keep_start  device int32 [seqs+1], non-decreasing, from 0
+ *   keep      device int32 [n]: positions
+ *   to        device int32 [seqs][width]: page tables that share no page with
+ *             `from`, nor with each other; or NULL: in place.  In place a
+ *             sequence's positions must ascend, and its pages be held by it
+ *             alone (as far as they are written)
+ * Positions and pages out of range are left out.  Errors as for dc_kv_copy
+ * (2^24 blocks of 64 tokens and 16 heads, or of a sequence in place).
+ */
+dc_status dc_kv_compact(const dc_kv_cache* layers, int32_t n_layers, const int32_t* from, int32_t seqs, int32_t width,
+                        const int32_t* keep_start, const int32_t* keep, int32_t n, const int32_t* to, void* stream);
+
+/*
+ * A matrix in microscaled 4-bit floating point (MXFP4): blocks of 32
+ * consecutive columns of a row share a scale 2^(s - 127), s a byte, and each
+ * element is an e2m1 code c (sign in bit 3): 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * Format: codes as bytes [ceil(rows/16)][cols/128][4][16][16]: piece (T, G, q, i)
+ * holds row 16T+i, columns 128G + 32q + e (e < 32), code e in the low (even e)
+ * or high half of byte e/2, so that the pieces of a tile are the lanes of a
+ * matrix-core operand; then scale bytes [ceil(rows/16)][ceil(cols/512)][4][16][4]:
+ * byte j of (T, H, q, i) is the scale of row 16T+i, columns 512H + 128j + 32q ..
+ * + 31.  What stands for rows past the last, and for columns past the last, is 0.
+ * rows: any number from 1; cols: a positive multiple of 128.  s = 255 makes a
+ * block NaN throughout.
+ */
+typedef struct dc_mx4_view {
+  int32_t rows, cols;
+  const void* base; /* device pointer to dc_mx4_bytes(rows, cols) bytes, 16-byte aligned */
+} dc_mx4_view;
+
+/* Size in bytes of the format; 0 if the shape is invalid. */
+size_t dc_mx4_bytes(int32_t rows, int32_t cols);
+
+/*
+ * dc_mx4_pack_device -- quantize bf16 rows into the format: s = max(0, e - 2)
+ * with e the exponent field of the block's largest magnitude (so s - 127 is
+ * floor(log2) - 2), codes the nearest of x / 2^(s - 127), ties to the even
+ * code, 6 for what is larger; the sign is kept.  A block with an infinity or a
+ * NaN gets s = 255.
+ *   X     device bf16 [rows][cols], rows `stride` elements apart (a multiple of 8)
+ *   dst   dst_bytes >= dc_mx4_bytes(rows, cols), fully written; must not
+ *         overlap X
+ *   flag  NULL, or device uint32: set to 0 by the call and to 1 if an entry is
+ *         not finite
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_BUFFER,
+ * DC_ERR_UNSUPPORTED (2^24 pieces of 64 rows and 512 columns or more).
+ * rows = 0 is a no-op.
+ */
+dc_status dc_mx4_pack_device(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, void* dst, size_t dst_bytes,
+                             uint32_t* flag, void* stream);
+
+/* dc_mx4_dequant -- what a matrix in the format stands for, exactly: X device
+ * bf16 [rows][cols], rows `stride` elements apart (a multiple of 8). */
+dc_status dc_mx4_dequant(const dc_mx4_view* w, uint16_t* X, int64_t stride, void* stream);
+
+/*
+ * dc_apply_mx4 -- y = W x for T tokens with bf16 activations (meant for few;
+ * any number is served): x device bf16 [T][cols], y device bf16 [T][rows].
+ * dc_apply_mx4q -- the same with the activations in the format too (quantize
+ * them with dc_mx4_pack_device): x is a view of [T][cols].  Products of 4-bit
+ * values are exact; for many tokens this is the fast form.
+ * Both: rows of W a multiple of 128; y fully overwritten, rounded once from
+ * fp32 sums in a fixed order; must not overlap x nor W.  A NaN block, or an x
+ * that is not finite, reaches its row and token only.
+ * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
+ * (2^31 entries of W or of x, or more than 1048560 tokens).
+ */
+dc_status dc_apply_mx4(const dc_mx4_view* w, const uint16_t* x, uint16_t* y, int32_t T, void* stream);
+dc_status dc_apply_mx4q(const dc_mx4_view* w, const dc_mx4_view* x, uint16_t* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,4 +16,7 @@ from ._lib import (  # noqa: F401
     DC_ERR_MAX_WIDTHS, dc_error_table, dc_error_table_workspace_bytes, dc_svd, dc_svd_workspace_bytes,
     DC_KV_BF16, DC_KV_E4M3, AttnBatch, KvCache, Rope, W4View, dc_apply_w4, dc_attention, dc_attention_workspace_bytes,
     dc_kv_append, dc_w4_bytes, dc_w4_pack_device,
+    DC_KV_BAD, DC_KV_FULL, DC_KV_MAX_LAYERS, DC_KV_MAX_SEQS, DC_LOGITS_BF16, DC_LOGITS_F32, KvLayers, KvTable, Mx4View,
+    VerifyBatch, dc_apply_mx4, dc_apply_mx4q, dc_kv_compact, dc_kv_copy, dc_kv_fork, dc_kv_resize, dc_mx4_bytes,
+    dc_mx4_dequant, dc_mx4_pack_device, dc_verify_drafts, dc_verify_workspace_bytes,
 )

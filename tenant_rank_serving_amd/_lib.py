@@ -39,14 +39,18 @@ EXPORTS = ("dc_status_string", "dc_check_spec", "dc_packed_bytes", "dc_algorithm
            "dc_apply_baseline_multitenant", "dc_apply_baseline_multitenant_group",
            "dc_error_table_workspace_bytes", "dc_error_table", "dc_svd_workspace_bytes", "dc_svd",
            "dc_kv_append", "dc_attention_workspace_bytes", "dc_attention", "dc_w4_bytes", "dc_w4_pack_device",
-           "dc_apply_w4")
+           "dc_apply_w4", "dc_verify_workspace_bytes", "dc_verify_drafts", "dc_kv_resize", "dc_kv_fork", "dc_kv_copy",
+           "dc_kv_compact", "dc_mx4_bytes", "dc_mx4_pack_device", "dc_mx4_dequant", "dc_apply_mx4", "dc_apply_mx4q")
 DC_ERR_MAX_WIDTHS = 8
 DC_KIND_LOWRANK, DC_KIND_BITDELTA = 1, 2
 DC_KV_BF16, DC_KV_E4M3 = 0, 1
+DC_LOGITS_BF16, DC_LOGITS_F32 = 0, 1
+DC_KV_FULL, DC_KV_BAD = 1, 2
+DC_KV_MAX_SEQS, DC_KV_MAX_LAYERS = 16384, 128
 _SIZE_FNS = ("dc_status_string", "dc_packed_bytes", "dc_algorithmic_bytes", "dc_workspace_bytes",
              "dc_group_workspace_bytes", "dc_baseline_bytes", "dc_baseline_algorithmic_bytes",
              "dc_baseline_workspace_bytes", "dc_error_table_workspace_bytes", "dc_svd_workspace_bytes",
-             "dc_attention_workspace_bytes", "dc_w4_bytes")
+             "dc_attention_workspace_bytes", "dc_w4_bytes", "dc_verify_workspace_bytes", "dc_mx4_bytes")
 STAGES = ("route", "xprep", "base", "vside", "uside")
 
 
@@ -91,6 +95,21 @@ class dc_attn_batch(ctypes.Structure):
 
 class dc_w4_view(ctypes.Structure):
     _fields_ = [("out", ctypes.c_int32), ("in_", ctypes.c_int32), ("base", ctypes.c_void_p)]
+
+
+class dc_verify_batch(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("q_start", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("accept", ctypes.c_void_p), ("pick", ctypes.c_void_p), ("temperature", ctypes.c_void_p)]
+
+
+class dc_kv_table(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("width", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("pages", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
+
+
+class dc_mx4_view(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("base", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -170,6 +189,20 @@ def lib() -> ctypes.CDLL:
         L.dc_w4_bytes.argtypes = [i32, i32]
         L.dc_w4_pack_device.argtypes = [i32, i32, _P, _P, ctypes.c_size_t, _P, _P]
         L.dc_apply_w4.argtypes = [ctypes.POINTER(dc_w4_view), _P, _P, i32, _P]
+        bp, tp, mp = ctypes.POINTER(dc_verify_batch), ctypes.POINTER(dc_kv_table), ctypes.POINTER(dc_mx4_view)
+        L.dc_verify_workspace_bytes.restype = ctypes.c_size_t
+        L.dc_verify_workspace_bytes.argtypes = [i32, i32, i32]
+        L.dc_verify_drafts.argtypes = [bp, i32, i32, _P, i64, _P, i64, i32, _P, _P, _P, _P, ctypes.c_size_t, _P]
+        L.dc_kv_resize.argtypes = [tp, _P, _P, _P, _P]
+        L.dc_kv_fork.argtypes = [tp, _P, _P, i32, _P, _P]
+        L.dc_kv_copy.argtypes = [kp, i32, _P, i32, _P]
+        L.dc_kv_compact.argtypes = [kp, i32, _P, i32, i32, _P, _P, i32, _P, _P]
+        L.dc_mx4_bytes.restype = ctypes.c_size_t
+        L.dc_mx4_bytes.argtypes = [i32, i32]
+        L.dc_mx4_pack_device.argtypes = [i32, i32, _P, i64, _P, ctypes.c_size_t, _P, _P]
+        L.dc_mx4_dequant.argtypes = [mp, _P, i64, _P]
+        L.dc_apply_mx4.argtypes = [mp, _P, _P, i32, _P]
+        L.dc_apply_mx4q.argtypes = [mp, mp, _P, _P]
         for name in EXPORTS:
             if name not in _SIZE_FNS:
                 getattr(L, name).restype = ctypes.c_int32
@@ -799,3 +832,191 @@ def dc_apply_w4(view: W4View, x, y, stream=None) -> None:
     if _rows(x, "x", t, view.inn, dev) != view.inn or _rows(y, "y", t, view.out, dev) != view.out:
         raise ValueError("x and y must be contiguous")
     _check(lib().dc_apply_w4(view.ref, _at(x), _at(y), t, _current(dev, stream)), "dc_apply_w4")
+
+
+# ------------------------------------------- verification of drafted tokens
+class VerifyBatch:
+    """The rows of a verification and its random numbers (keeps its tensors
+    alive; see dc_verify_batch): q_start int32 [B+1], tokens int32 [N], accept
+    fp32 [N], pick fp32 [B], temperature fp32 [B] or None (1)."""
+
+    def __init__(self, q_start, tokens, accept, pick, temperature=None):
+        i32, f32 = ("int32",), ("float32",)
+        self.seqs, self.n = pick.numel(), tokens.numel()
+        for t, what, names, n in ((q_start, "q_start", i32, self.seqs + 1), (tokens, "tokens", i32, self.n),
+                                  (accept, "accept", f32, self.n), (pick, "pick", f32, self.seqs),
+                                  (temperature, "temperature", f32, self.seqs)):
+            if t is not None and (_typed(t, what, names).dim() != 1 or t.numel() != n):
+                raise ValueError("%s must be [%d]" % (what, n))
+        self.device = q_start.get_device()
+        _same_device(self.device, tokens=tokens, accept=accept, pick=pick, temperature=temperature)
+        self._keep = (q_start, tokens, accept, pick, temperature)
+        self.c = dc_verify_batch(self.seqs, int(q_start.data_ptr()), _at(tokens), _at(accept), _at(pick),
+                                 None if temperature is None else _at(temperature))
+        self.ref = ctypes.byref(self.c)
+
+
+def dc_verify_workspace_bytes(vocab: int, n: int, seqs: int) -> int:
+    return int(lib().dc_verify_workspace_bytes(int(vocab), int(n), int(seqs)))
+
+
+def _logits(t, what: str, n: int, vocab: int, dtype, device: int) -> int:
+    """The row stride of logits [n][vocab]."""
+    if t.shape != (n, vocab) or t.dtype != dtype or t.get_device() != device:
+        raise ValueError("%s must be %s [%d][%d] on device %d" % (what, dtype, n, vocab, device))
+    stride, one = t.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("the rows of %s must be contiguous" % what)
+    return stride if n > 1 else vocab
+
+
+def dc_verify_drafts(batch: VerifyBatch, target, draft, out, count, ws, prob=None, stream=None) -> None:
+    """Which drafted tokens stand, and the new token of each sequence: target
+    (and draft, or None) [N][vocab] bf16 or fp32 logits, rows of any stride;
+    out int32 [N], count int32 [B], prob fp32 [N] or None."""
+    t = _torch or _load_torch()
+    dev, n, vocab = batch.device, batch.n, target.shape[1]
+    kind = {t.bfloat16: DC_LOGITS_BF16, t.float32: DC_LOGITS_F32}.get(target.dtype)
+    if kind is None:
+        raise ValueError("target must be bf16 or fp32, not %s" % target.dtype)
+    ts = _logits(target, "target", n, vocab, target.dtype, dev)
+    ds = _logits(draft, "draft", n, vocab, target.dtype, dev) if draft is not None else 0
+    po, pc = _vector(out, "out", n, t.int32, dev), _vector(count, "count", batch.seqs, t.int32, dev)
+    pp = None if prob is None else _vector(prob, "prob", n, t.float32, dev)
+    if ws.get_device() != dev:
+        raise ValueError("the workspace must be on device %d" % dev)
+    _check(lib().dc_verify_drafts(batch.ref, kind, vocab, _at(target), ts, None if draft is None else _at(draft), ds, n, po,
+                                  pc, pp, _dptr(ws, "ws"), ws.numel() * ws.element_size(), _current(dev, stream)),
+           "dc_verify_drafts")
+
+
+# ------------------------------------------------- page tables and pages
+class KvTable:
+    """Page tables of a cache's sequences (keeps its tensors alive; see
+    dc_kv_table): pages int32 [B][width], kv_len int32 [B], refs int32
+    [num_pages], page: tokens of a page."""
+
+    def __init__(self, pages, kv_len, refs, page: int):
+        i32 = ("int32",)
+        if _typed(pages, "pages", i32).dim() != 2 or _typed(kv_len, "kv_len", i32).shape != (pages.shape[0],) or \
+                _typed(refs, "refs", i32).dim() != 1:
+            raise ValueError("pages must be [B][width], kv_len [B] and refs [num_pages]")
+        self.device = pages.get_device()
+        _same_device(self.device, kv_len=kv_len, refs=refs)
+        self._keep = (pages, kv_len, refs)
+        self.seqs, self.width = pages.shape
+        self.c = dc_kv_table(self.seqs, self.width, int(page), refs.numel(), _at(pages), _at(kv_len), _at(refs))
+        self.ref = ctypes.byref(self.c)
+
+
+def dc_kv_resize(table: KvTable, new_len, copies, status, stream=None) -> None:
+    """Sequences take the lengths new_len int32 [B]: pages are given back and
+    taken; copies int32 [B][2] is written (pairs for dc_kv_copy), bits are or-ed
+    into status int32 [1]."""
+    i32 = (_torch or _load_torch()).int32
+    dev = table.device
+    if copies.shape != (table.seqs, 2):
+        raise ValueError("copies must be [%d][2]" % table.seqs)
+    _check(lib().dc_kv_resize(table.ref, _vector(new_len, "new_len", table.seqs, i32, dev),
+                              _vector(copies.view(-1), "copies", 2 * table.seqs, i32, dev),
+                              _vector(status, "status", 1, i32, dev), _current(dev, stream)), "dc_kv_resize")
+
+
+def dc_kv_fork(table: KvTable, src, dst, status, stream=None) -> None:
+    """Rows dst (int32 [n]) become branches of rows src (int32 [n])."""
+    i32 = (_torch or _load_torch()).int32
+    dev, n = table.device, src.numel()
+    _check(lib().dc_kv_fork(table.ref, _vector(src, "src", n, i32, dev), _vector(dst, "dst", n, i32, dev), n,
+                            _vector(status, "status", 1, i32, dev), _current(dev, stream)), "dc_kv_fork")
+
+
+class KvLayers:
+    """The caches of a model's layers, numbered alike (keeps them alive)."""
+
+    def __init__(self, caches):
+        self._keep = list(caches)
+        if not self._keep:
+            raise ValueError("at least one layer")
+        self.device = self._keep[0].device
+        if any(c.device != self.device for c in self._keep):
+            raise ValueError("the layers must be on one device")
+        self.n = len(self._keep)
+        self.c = (dc_kv_cache * self.n)(*[c.c for c in self._keep])
+
+
+def dc_kv_copy(layers: KvLayers, copies, stream=None) -> None:
+    """Whole pages of all layers: copies int32 [n][2], from and to."""
+    i32 = (_torch or _load_torch()).int32
+    n, dev = copies.shape[0], layers.device
+    if copies.shape != (n, 2):
+        raise ValueError("copies must be [n][2]")
+    _check(lib().dc_kv_copy(layers.c, layers.n, _vector(copies.view(-1), "copies", 2 * n, i32, dev), n,
+                            _current(dev, stream)), "dc_kv_copy")
+
+
+def dc_kv_compact(layers: KvLayers, from_pages, keep_start, keep, to_pages=None, stream=None) -> None:
+    """Sequences keep the tokens at positions keep (int32 [n]; sequence b's are
+    keep_start[b] .. keep_start[b+1]-1 of it): moved within from_pages int32
+    [B][width] (None), or to to_pages."""
+    i32 = (_torch or _load_torch()).int32
+    dev, n = layers.device, keep.numel()
+    b, width = from_pages.shape
+    if to_pages is not None and to_pages.shape != (b, width):
+        raise ValueError("to_pages must be [%d][%d]" % (b, width))
+    _check(lib().dc_kv_compact(layers.c, layers.n, _vector(from_pages.view(-1), "from_pages", b * width, i32, dev), b, width,
+                               _vector(keep_start, "keep_start", b + 1, i32, dev), _vector(keep, "keep", n, i32, dev), n,
+                               None if to_pages is None else _vector(to_pages.view(-1), "to_pages", b * width, i32, dev),
+                               _current(dev, stream)), "dc_kv_compact")
+
+
+# ----------------------------------------------- microscaled 4-bit matrices
+def dc_mx4_bytes(rows: int, cols: int) -> int:
+    return int(lib().dc_mx4_bytes(int(rows), int(cols)))
+
+
+class Mx4View:
+    """A matrix [rows][cols] in microscaled 4-bit floating point (keeps its
+    tensor alive)."""
+
+    def __init__(self, rows: int, cols: int, buf):
+        need = dc_mx4_bytes(rows, cols)
+        if not need or not buf.is_contiguous() or buf.numel() * buf.element_size() < need:
+            raise ValueError("the buffer must be contiguous and hold the matrix (%d bytes; 0: no such shape)" % need)
+        self.rows, self.cols, self.buf, self.device = int(rows), int(cols), buf, buf.get_device()
+        self.c = dc_mx4_view(self.rows, self.cols, int(buf.data_ptr()))
+        self.ref = ctypes.byref(self.c)
+
+
+def dc_mx4_pack_device(X, view: Mx4View, flag=None, stream=None) -> None:
+    """Quantize X (bf16 [rows][cols], rows of any stride) into the view's buffer;
+    flag int32/uint32 [1] or None."""
+    dev = view.device
+    xs = _rows(X, "X", view.rows, view.cols, dev)
+    if flag is not None:
+        _typed(flag, "flag", ("int32", "uint32"))
+        _same_device(dev, flag=flag)
+    _check(lib().dc_mx4_pack_device(view.rows, view.cols, _at(X), xs, view.buf.data_ptr(),
+                                    view.buf.numel() * view.buf.element_size(), _dptr(flag, "flag"), _current(dev, stream)),
+           "dc_mx4_pack_device")
+
+
+def dc_mx4_dequant(view: Mx4View, X, stream=None) -> None:
+    """What the matrix stands for: X bf16 [rows][cols], rows of any stride."""
+    xs = _rows(X, "X", view.rows, view.cols, view.device)
+    _check(lib().dc_mx4_dequant(view.ref, _at(X), xs, _current(view.device, stream)), "dc_mx4_dequant")
+
+
+def dc_apply_mx4(view: Mx4View, x, y, stream=None) -> None:
+    """y [T][rows] = W x, x [T][cols], both bf16 and contiguous."""
+    t, dev = x.shape[0], view.device
+    if _rows(x, "x", t, view.cols, dev) != view.cols or _rows(y, "y", t, view.rows, dev) != view.rows:
+        raise ValueError("x and y must be contiguous")
+    _check(lib().dc_apply_mx4(view.ref, _at(x), _at(y), t, _current(dev, stream)), "dc_apply_mx4")
+
+
+def dc_apply_mx4q(view: Mx4View, x: Mx4View, y, stream=None) -> None:
+    """y [T][rows] = W x with x [T][cols] in the format too; y bf16, contiguous."""
+    dev = view.device
+    if x.device != dev or _rows(y, "y", x.rows, view.rows, dev) != view.rows:
+        raise ValueError("x must be on device %d and y contiguous" % dev)
+    _check(lib().dc_apply_mx4q(view.ref, x.ref, _at(y), _current(dev, stream)), "dc_apply_mx4q")

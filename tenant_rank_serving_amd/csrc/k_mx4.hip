@@ -1,0 +1,247 @@
+// Microscaled 4-bit floating point (MXFP4): the packer, its inverse, and
+// products with bf16 or MXFP4 activations.
+//
+// y_t[o] = sum over blocks B of 32 columns of 2^(s_oB - 127) sum_{k in B} c_ok x_tk.
+// A lane's piece is one block of one row, so the conversions take the block's
+// scale as their operand (bf16 activations: v_cvt_scalef32_pk_bf16_fp4, exact),
+// and so does the matrix core (MXFP4 activations: v_mfma_scale, products exact,
+// sums fp32).
+#include <hip/hip_runtime.h>
+
+#include "step.h"
+
+namespace dc {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kFp4 = 4;   // the matrix core's format number
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+// The scale byte as the fp32 number whose exponent field it is: the conversions
+// read that field (0: 2^-127), and 255 has to be NaN, not infinity.
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte == 255 ? 0x7FC00000u : byte << 23);
+}
+
+// 8 codes as bf16.
+__device__ __forceinline__ bf16x8 codes8(uint32_t w, float s) {
+  uint4 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ v8i piece(uint4 w) { return v8i{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0}; }
+
+// ------------------------------------------------------------------ packer
+// A wave takes 16 rows x 512 columns, lane l row l%16 and block l/16 of each
+// 128 columns: loads are 256 bytes of a row, stores whole KiB of codes.
+__global__ void __launch_bounds__(256) k_mx4_pack(const uint16_t* __restrict__ X, int64_t stride, uint8_t* __restrict__ dst,
+                                                  uint32_t* __restrict__ flag, int rows, int cols) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int gc = cols / 128, hc = (gc + 3) / 4;
+  const int T = blockIdx.x / hc * 4 + wave, H = blockIdx.x % hc;
+  if (T * 16 >= rows) return;
+  const int row = T * 16 + (lane & 15);
+  const bool have = row < rows;
+  const uint16_t* src = X + (int64_t)(have ? row : rows - 1) * stride + 512 * H + 32 * (lane >> 4);
+  uint4 x[4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int g = min(4 * H + j, gc - 1) - 4 * H;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[j][i] = *reinterpret_cast<const uint4*>(src + 128 * g + 8 * i);
+  }
+  uint32_t scales = 0;
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (4 * H + j >= gc) break;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u[4] = {x[j][i].x, x[j][i].y, x[j][i].z, x[j][i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = max2(m, u[e] & 0x7FFF7FFFu);
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    const uint32_t ex = m >> 7;   // the exponent field of the largest
+    uint32_t s = ex > 2 ? ex - 2 : 0;
+    if (ex == 255) s = 255, bad |= have;
+    uint32_t w[4];
+    const float f = __uint_as_float(s << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t r = 0;
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x[j][i].x), f, 0);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x[j][i].y), f, 1);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x[j][i].z), f, 2);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, x[j][i].w), f, 3);
+      w[i] = have && ex < 255 ? r : 0u;
+    }
+    scales |= (have ? s : 0u) << (8 * j);
+    *reinterpret_cast<uint4*>(dst + ((size_t)T * gc + 4 * H + j) * 1024 + lane * 16) = uint4{w[0], w[1], w[2], w[3]};
+  }
+  const size_t codes = (size_t)((rows + 15) / 16) * gc * 1024;
+  *reinterpret_cast<uint32_t*>(dst + codes + ((size_t)T * hc + H) * 256 + lane * 4) = scales;
+  if (bad && flag) atomicOr(flag, 1u);
+}
+
+__global__ void k_mx4_flag(uint32_t* flag) { *flag = 0; }
+
+// The same tiles the other way.
+__global__ void __launch_bounds__(256) k_mx4_dequant(const uint8_t* __restrict__ w, uint16_t* __restrict__ X, int64_t stride,
+                                                     int rows, int cols) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int gc = cols / 128, hc = (gc + 3) / 4;
+  const int T = blockIdx.x / hc * 4 + wave, H = blockIdx.x % hc;
+  if (T * 16 >= rows) return;
+  const int row = T * 16 + (lane & 15);
+  const size_t codes = (size_t)((rows + 15) / 16) * gc * 1024;
+  const uint32_t scales = *reinterpret_cast<const uint32_t*>(w + codes + ((size_t)T * hc + H) * 256 + lane * 4);
+  uint16_t* dst = X + (int64_t)row * stride + 512 * H + 32 * (lane >> 4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (4 * H + j >= gc) break;
+    const uint4 c = *reinterpret_cast<const uint4*>(w + ((size_t)T * gc + 4 * H + j) * 1024 + lane * 16);
+    const float s = scale_of(scales >> (8 * j) & 255u);
+    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+    if (row < rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(dst + 128 * j + 8 * i) = __builtin_bit_cast(uint4, codes8(u[i], s));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+// Block: RT 16-row tiles of the matrix x TT 16-token tiles, all columns; NW
+// waves take the 512-column groups in turn and add their sums through LDS: one
+// launch, no workspace.  Lane l holds row (token) l%16 and block l/16 of 128
+// columns; result: token l%16, rows 4(l/16) .. +4.
+template <int RT, int TT, int NW, bool XQ>
+__global__ void __launch_bounds__(64 * NW, NW / 4) k_mx4(Mx4Args a) {
+  __shared__ float red[NW][RT * 16][TT * 16 + 1];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int r0 = blockIdx.x * RT, t0 = blockIdx.y * TT;   // first tiles
+  const int gc = a.in / 128, hc = (gc + 3) / 4, rts = a.out / 16, tts = (a.T + 15) / 16;
+  const uint8_t* ws = a.w + (size_t)rts * gc * 1024;
+  const uint8_t* xs = a.xq + (size_t)tts * gc * 1024;
+  f32x4 acc[RT][TT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int g = wave; g < gc; g += NW) {
+    const int H = g >> 2, j8 = 8 * (g & 3);
+    uint4 w[RT];
+    uint32_t s[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const size_t T = min(r0 + r, rts - 1);
+      w[r] = *reinterpret_cast<const uint4*>(a.w + (T * gc + g) * 1024 + lane * 16);
+      s[r] = *reinterpret_cast<const uint32_t*>(ws + (T * hc + H) * 256 + lane * 4) >> j8 & 255u;
+    }
+    if constexpr (XQ) {
+      uint4 x[TT];
+      uint32_t xsc[TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const size_t T = min(t0 + t, tts - 1);
+        x[t] = *reinterpret_cast<const uint4*>(a.xq + (T * gc + g) * 1024 + lane * 16);
+        xsc[t] = *reinterpret_cast<const uint32_t*>(xs + (T * hc + H) * 256 + lane * 4) >> j8 & 255u;
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          acc[r][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(piece(w[r]), piece(x[t]), acc[r][t], kFp4, kFp4, 0,
+                                                                      (int)s[r], 0, (int)xsc[t]);
+    } else {
+      bf16x8 b[TT][4];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const uint16_t* xp = a.x + (size_t)min(16 * (t0 + t) + (lane & 15), a.T - 1) * a.in + 128 * g + 32 * (lane >> 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[t][j] = *reinterpret_cast<const bf16x8*>(xp + 8 * j);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float f = scale_of(s[r]);
+        const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 c = codes8(u[j], f);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) acc[r][t] = mfma(c, b[t][j], acc[r][t]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[wave][16 * r + 4 * (lane >> 4) + i][16 * t + (lane & 15)] = acc[r][t][i];
+  __syncthreads();
+  for (int e = tid; e < RT * 16 * TT * 16; e += 64 * NW) {   // consecutive threads: consecutive rows of a token
+    const int row = e % (RT * 16), tok = e / (RT * 16);
+    float v = 0.f;
+#pragma unroll
+    for (int n = 0; n < NW; ++n) v += red[n][row][tok];
+    if (16 * t0 + tok < a.T && 16 * r0 + row < a.out)
+      a.y[(size_t)(16 * t0 + tok) * a.out + 16 * r0 + row] = __builtin_bit_cast(uint16_t, (__bf16)v);
+  }
+}
+
+template <int RT, int TT, bool XQ>
+void go(const Mx4Args& a) {
+  const dim3 g((unsigned)((a.out / 16 + RT - 1) / RT), (unsigned)((a.T + TT * 16 - 1) / (TT * 16)));
+  hipLaunchKernelGGL((k_mx4<RT, TT, 8, XQ>), g, dim3(512), 0, reinterpret_cast<hipStream_t>(a.stream), a);
+}
+
+}  // namespace
+
+int launch_mx4(const Mx4Args& a) {
+  if (a.T <= 16) go<1, 1, false>(a);
+  else go<4, 2, false>(a);
+  return (int)hipGetLastError();
+}
+
+int launch_mx4q(const Mx4Args& a) {
+  if (a.T <= 16) go<1, 1, true>(a);
+  else go<4, 2, true>(a);
+  return (int)hipGetLastError();
+}
+
+int launch_mx4_pack(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, uint8_t* dst, uint32_t* flag,
+                    void* stream) {
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (flag) hipLaunchKernelGGL(k_mx4_flag, dim3(1), dim3(1), 0, st, flag);
+  const unsigned g = (unsigned)((rows + 63) / 64) * (unsigned)((cols + 511) / 512);
+  hipLaunchKernelGGL(k_mx4_pack, dim3(g), dim3(256), 0, st, X, stride, dst, flag, rows, cols);
+  return (int)hipGetLastError();
+}
+
+int launch_mx4_dequant(int32_t rows, int32_t cols, const uint8_t* w, uint16_t* X, int64_t stride, void* stream) {
+  const unsigned g = (unsigned)((rows + 63) / 64) * (unsigned)((cols + 511) / 512);
+  hipLaunchKernelGGL(k_mx4_dequant, dim3(g), dim3(256), 0, reinterpret_cast<hipStream_t>(stream), w, X, stride, rows, cols);
+  return (int)hipGetLastError();
+}
+
+}  // namespace dc

@@ -1,0 +1,369 @@
+// Page tables of a cache's sequences, and pages: forking, growing and giving
+// back, copying, compacting.
+//
+// The tables are a few thousand numbers, whose order matters (free pages go out
+// lowest first, to the sequences in order): one block keeps them, so that a
+// captured step needs no host.  Copies move bytes: every piece of 16 bytes is
+// read and written once, blocks over pages (or tokens), layers, keys and values.
+#include <hip/hip_runtime.h>
+
+#include "step.h"
+
+namespace dc {
+namespace {
+
+// ------------------------------------------------------------------ tables
+constexpr int kResizeThreads = 1024, kWaves = kResizeThreads / 64;
+
+__device__ __forceinline__ int32_t ld_agent(const int32_t* p) {
+  return __hip_atomic_load(const_cast<int32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void add_agent(int32_t* p, int32_t v) {
+  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What a block's 16 waves hold, added up for the waves before this one and in
+// all; `box` [16].
+__device__ __forceinline__ int before_wave(int mine, int* box, int* all) {
+  const int wave = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) box[wave] = mine;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const int v = box[w];
+    before += w < wave ? v : 0;
+    sum += v;
+  }
+  *all = sum;
+  return before;
+}
+
+__device__ __forceinline__ int upto_lane(int v) {
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const int o = __shfl_up(v, x);
+    if ((int)(threadIdx.x & 63) >= x) v += o;
+  }
+  return v;
+}
+
+// One block.  Pages behind the new lengths are given back; then each sequence's
+// need is known, and the free pages, in the order of their numbers, are dealt
+// to the sequences, in theirs: the k-th one to the sequence among whose running
+// needs k falls.
+__global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const int32_t* new_len, int32_t* copies) {
+  // per sequence: pages needed up to and with it, and whether the first of its own is for an exchange
+  __shared__ uint32_t upto[DC_KV_MAX_SEQS];
+  __shared__ int box[kWaves];
+  __shared__ uint32_t status;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int most = t.width * t.page, shift = 31 - __builtin_clz(t.page);
+  auto pages_of = [&](int n) { return (int)(((int64_t)n + t.page - 1) >> shift); };
+  if (tid == 0) status = 0;
+  __syncthreads();
+
+  for (int b = wave; b < t.seqs; b += kWaves) {
+    const int old = t.kv_len[b], want = new_len[b];
+    if (old < 0 || old > most || want < 0 || want > most) {
+      if (lane == 0) atomicOr(&status, (uint32_t)DC_KV_BAD);
+      continue;
+    }
+    int32_t* row = t.pages + (int64_t)b * t.width;
+    for (int i = pages_of(want) + lane; i < pages_of(old); i += 64) {
+      const int32_t p = row[i];
+      if (p >= 0 && p < t.num_pages) add_agent(t.refs + p, -1);
+      else atomicOr(&status, (uint32_t)DC_KV_BAD);
+      row[i] = -1;
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // the counts have fallen
+  __syncthreads();
+
+  int total = 0;
+  for (int b0 = 0; b0 < t.seqs; b0 += kResizeThreads) {
+    const int b = b0 + tid;
+    int need = 0;
+    bool swap = false;
+    if (b < t.seqs) {
+      const int old = t.kv_len[b], want = new_len[b];
+      if (old >= 0 && old <= most && want > old && want <= most) {
+        need = pages_of(want) - pages_of(old);
+        if (old & (t.page - 1)) {
+          const int32_t p = t.pages[(int64_t)b * t.width + (old >> shift)];
+          if (p >= 0 && p < t.num_pages) swap = ld_agent(t.refs + p) > 1;
+          else atomicOr(&status, (uint32_t)DC_KV_BAD);
+          need += swap;
+        }
+      }
+      copies[2 * b] = copies[2 * b + 1] = -1;
+    }
+    const int sum = upto_lane(need);
+    int all;
+    const int before = before_wave(__shfl(sum, 63), box, &all);
+    if (b < t.seqs) upto[b] = (uint32_t)(total + before + sum) << 1 | (uint32_t)swap;
+    total += all;
+  }
+  __syncthreads();
+
+  // the free pages: 4 a thread, the next ones on their way while these are dealt
+  int dealt = 0;
+  const int vecs = (t.num_pages + 3) / 4;
+  auto load = [&](int v) {
+    int4 r = int4{1, 1, 1, 1};
+    if (4 * v + 3 < t.num_pages) r = reinterpret_cast<const int4*>(t.refs)[v];
+    else if (v < vecs) {
+      r.x = t.refs[4 * v];
+      if (4 * v + 1 < t.num_pages) r.y = t.refs[4 * v + 1];
+      if (4 * v + 2 < t.num_pages) r.z = t.refs[4 * v + 2];
+    }
+    return r;
+  };
+  // (the counts that fell are in the L2; nothing of them is in this CU's L1 yet)
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  int4 now = load(tid), next = load(kResizeThreads + tid);
+  for (int v0 = 0; v0 < vecs && dealt < total; v0 += kResizeThreads) {
+    const int4 later = load(v0 + 2 * kResizeThreads + tid);
+    const int r[4] = {now.x, now.y, now.z, now.w};
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine += r[j] <= 0;
+    const int sum = upto_lane(mine);
+    int all;
+    int k = dealt + before_wave(__shfl(sum, 63), box, &all) + sum - mine;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (r[j] > 0) continue;
+      if (k < total) {
+        const int32_t p = 4 * (v0 + tid) + j;
+        int lo = 0, hi = t.seqs - 1;   // the first sequence with upto > k
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if ((int)(upto[mid] >> 1) > k) hi = mid; else lo = mid + 1;
+        }
+        const int slot = k - (lo ? (int)(upto[lo - 1] >> 1) : 0);
+        const bool swap = upto[lo] & 1;
+        const int old = t.kv_len[lo];
+        int32_t* row = t.pages + (int64_t)lo * t.width;
+        if (swap && slot == 0) {
+          copies[2 * lo] = row[old >> shift];
+          copies[2 * lo + 1] = p;
+          row[old >> shift] = p;
+        } else {
+          row[pages_of(old) + slot - swap] = p;
+        }
+        t.refs[p] = 1;
+      }
+      ++k;
+    }
+    dealt += all;
+    now = next;
+    next = later;
+  }
+  const int have = dealt < total ? dealt : total;
+  __syncthreads();
+
+  for (int b0 = 0; b0 < t.seqs; b0 += kResizeThreads) {
+    const int b = b0 + tid;
+    if (b >= t.seqs) continue;
+    const int old = t.kv_len[b], want = new_len[b];
+    if (old < 0 || old > most || want < 0 || want > most) continue;
+    const int end = (int)(upto[b] >> 1), first = b ? (int)(upto[b - 1] >> 1) : 0;
+    const bool swap = upto[b] & 1;
+    if (end > first && end > have) {   // too few: what it was dealt goes back
+      atomicOr(&status, (uint32_t)DC_KV_FULL);
+      int32_t* row = t.pages + (int64_t)b * t.width;
+      for (int k = first; k < have; ++k) {
+        const int slot = k - first;
+        if (swap && slot == 0) {
+          t.refs[copies[2 * b + 1]] = 0;
+          row[old >> shift] = copies[2 * b];
+          copies[2 * b] = copies[2 * b + 1] = -1;
+        } else {
+          int32_t* e = row + pages_of(old) + slot - swap;
+          t.refs[*e] = 0;
+          *e = -1;
+        }
+      }
+      continue;
+    }
+    if (swap) add_agent(t.refs + copies[2 * b], -1);
+    t.kv_len[b] = want;
+  }
+  __syncthreads();
+  if (tid == 0 && status) atomicOr(t.status, status);
+}
+
+// Block: one branch.
+__global__ void __launch_bounds__(256) k_fork(TableArgs t, const int32_t* src, const int32_t* dst) {
+  const int s = src[blockIdx.x], d = dst[blockIdx.x], tid = threadIdx.x;
+  bool ok = s >= 0 && s < t.seqs && d >= 0 && d < t.seqs && s != d;
+  int n = 0;
+  if (ok) {
+    n = t.kv_len[s];
+    ok = n >= 0 && n <= t.width * t.page && t.kv_len[d] == 0;
+  }
+  __syncthreads();   // everyone has read the lengths
+  if (!ok) {
+    if (tid == 0) atomicOr(t.status, (uint32_t)DC_KV_BAD);
+    return;
+  }
+  const int32_t* from = t.pages + (int64_t)s * t.width;
+  int32_t* to = t.pages + (int64_t)d * t.width;
+  const int pages = (int)(((int64_t)n + t.page - 1) / t.page);
+  bool bad = false;
+  for (int i = tid; i < pages; i += 256) {
+    const int32_t p = from[i];
+    to[i] = p;
+    if (p >= 0 && p < t.num_pages) add_agent(t.refs + p, 1);
+    else bad = true;
+  }
+  if (bad) atomicOr(t.status, (uint32_t)DC_KV_BAD);
+  if (tid == 0) t.kv_len[d] = n;
+}
+
+// -------------------------------------------------------------------- copy
+__device__ __forceinline__ uint8_t* pool_of(const LayerArgs& a, int lv) {
+  return lv & 1 ? a.v[lv >> 1] : a.k[lv >> 1];
+}
+
+// Piece u of a page, in the order of memory: rows of a head, or heads of a row.
+__device__ __forceinline__ int64_t piece_at(const LayerArgs& a, int u) {
+  const int c = u & ((1 << a.pieces) - 1), r = u >> a.pieces;
+  int h, s;
+  if (a.slot_stride <= a.head_stride) h = r >> a.shift, s = r & ((1 << a.shift) - 1);
+  else s = r / a.heads, h = r - s * a.heads;
+  return h * a.head_stride + s * a.slot_stride + 16 * c;
+}
+
+// Block: 16 KiB of a page of one layer's keys or values.
+__global__ void __launch_bounds__(256) k_copy(LayerArgs a, const int32_t* copies) {
+  const int64_t from = copies[2 * blockIdx.x], to = copies[2 * blockIdx.x + 1];
+  if (from < 0 || from >= a.num_pages || to < 0 || to >= a.num_pages || from == to) return;
+  uint8_t* pool = pool_of(a, blockIdx.y);
+  const int pieces = a.heads << (a.shift + a.pieces), u0 = blockIdx.z * kCopyBlock + threadIdx.x;
+  uint4 x[kCopyBlock / 256];
+#pragma unroll
+  for (int i = 0; i < kCopyBlock / 256; ++i) {
+    const int u = u0 + 256 * i;
+    if (u < pieces) x[i] = *reinterpret_cast<const uint4*>(pool + from * a.page_stride + piece_at(a, u));
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyBlock / 256; ++i) {
+    const int u = u0 + 256 * i;
+    if (u < pieces) *reinterpret_cast<uint4*>(pool + to * a.page_stride + piece_at(a, u)) = x[i];
+  }
+}
+
+// ----------------------------------------------------------------- compact
+// Byte offset of a token of a sequence, -1 if there is none.
+__device__ __forceinline__ int64_t token_at(const LayerArgs& a, const int32_t* table, int width, int seq, int pos) {
+  if (pos < 0 || (pos >> a.shift) >= width) return -1;
+  const int32_t p = table[(int64_t)seq * width + (pos >> a.shift)];
+  if (p < 0 || p >= a.num_pages) return -1;
+  return p * a.page_stride + (pos & ((1 << a.shift) - 1)) * a.slot_stride;
+}
+
+// Block: 64 kept tokens, 16 heads of one layer's keys or values.  To other
+// pages the blocks are independent (`tiles` of them); in place one block moves
+// a sequence's tokens, 64 at a time: sources ascend and lie at or behind their
+// places, so a tile's places hold nothing that is still to be read once the
+// tile itself has been.
+template <bool InPlace>
+__global__ void __launch_bounds__(256) k_compact(LayerArgs a, const int32_t* from, const int32_t* to,
+                                                 const int32_t* start, const int32_t* keep, int seqs, int width, int n) {
+  __shared__ int64_t src[kCompactTokens], dst[kCompactTokens];
+  const int tid = threadIdx.x;
+  uint8_t* pool = pool_of(a, blockIdx.y);
+  const int h0 = blockIdx.z * kCompactHeads, heads = min(kCompactHeads, a.heads - h0);
+  const int log_units = 6 + a.pieces;   // of a head's tile
+  int t0, t1, seq0 = 0;
+  if constexpr (InPlace) {
+    seq0 = blockIdx.x;
+    t0 = min(max(start[seq0], 0), n);
+    t1 = min(start[seq0 + 1], n);
+  } else {
+    t0 = blockIdx.x * kCompactTokens;
+    t1 = min(t0 + kCompactTokens, n);
+  }
+  for (int tile = t0; tile < t1; tile += kCompactTokens) {
+    if (tid < kCompactTokens) {
+      const int j = tile + tid;
+      int64_t s = -1, d = -1;
+      if (j < t1) {
+        int seq = seq0;
+        if constexpr (!InPlace) {   // the last sequence that starts at or before j
+          int lo = 0, hi = seqs;
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= j) lo = mid + 1; else hi = mid;
+          }
+          seq = lo - 1;
+        }
+        if (seq >= 0 && j < start[seq + 1]) {
+          s = token_at(a, from, width, seq, keep[j]);
+          d = token_at(a, InPlace ? from : to, width, seq, j - max(start[seq], 0));
+        }
+      }
+      src[tid] = s != d && d >= 0 ? s : -1;   // (in place: where it is already)
+      dst[tid] = d;
+    }
+    __syncthreads();
+    constexpr int kUnits = 16;   // a thread's pieces at a time
+    for (int u0 = 0; u0 < (heads << log_units); u0 += 256 * kUnits) {
+      uint4 x[kUnits];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = u0 + 256 * i + tid, h = u >> log_units, tok = (u >> a.pieces) & (kCompactTokens - 1);
+        if (h >= heads || src[tok] < 0) continue;
+        x[i] = *reinterpret_cast<const uint4*>(pool + src[tok] + (h0 + h) * a.head_stride + 16 * (u & ((1 << a.pieces) - 1)));
+      }
+      if constexpr (InPlace) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();   // every piece of these heads' tile has been read
+      }
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int u = u0 + 256 * i + tid, h = u >> log_units, tok = (u >> a.pieces) & (kCompactTokens - 1);
+        if (h >= heads || src[tok] < 0) continue;
+        *reinterpret_cast<uint4*>(pool + dst[tok] + (h0 + h) * a.head_stride + 16 * (u & ((1 << a.pieces) - 1))) = x[i];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+int launch_resize(const TableArgs& t, const int32_t* new_len, int32_t* copies) {
+  hipLaunchKernelGGL(k_resize, dim3(1), dim3(kResizeThreads), 0, reinterpret_cast<hipStream_t>(t.stream), t, new_len, copies);
+  return (int)hipGetLastError();
+}
+
+int launch_fork(const TableArgs& t, const int32_t* src, const int32_t* dst, int32_t n) {
+  hipLaunchKernelGGL(k_fork, dim3((unsigned)n), dim3(256), 0, reinterpret_cast<hipStream_t>(t.stream), t, src, dst);
+  return (int)hipGetLastError();
+}
+
+int launch_copy(const LayerArgs& a, const int32_t* copies, int32_t n, void* stream) {
+  const unsigned parts = (unsigned)(((a.heads << (a.shift + a.pieces)) + kCopyBlock - 1) / kCopyBlock);
+  hipLaunchKernelGGL(k_copy, dim3((unsigned)n, 2u * (unsigned)a.layers, parts), dim3(256), 0,
+                     reinterpret_cast<hipStream_t>(stream), a, copies);
+  return (int)hipGetLastError();
+}
+
+int launch_compact(const LayerArgs& a, const int32_t* from, const int32_t* to, const int32_t* start,
+                   const int32_t* keep, int32_t seqs, int32_t width, int32_t n, void* stream) {
+  const unsigned groups = (unsigned)((a.heads + kCompactHeads - 1) / kCompactHeads);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (to)
+    hipLaunchKernelGGL(k_compact<false>, dim3((unsigned)((n + kCompactTokens - 1) / kCompactTokens), 2u * (unsigned)a.layers, groups),
+                       dim3(256), 0, st, a, from, to, start, keep, seqs, width, n);
+  else
+    hipLaunchKernelGGL(k_compact<true>, dim3((unsigned)seqs, 2u * (unsigned)a.layers, groups), dim3(256), 0, st, a, from,
+                       from, start, keep, seqs, width, n);
+  return (int)hipGetLastError();
+}
+
+}  // namespace dc
