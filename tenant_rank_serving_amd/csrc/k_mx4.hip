@@ -223,9 +223,35 @@ int launch_mx4(const Mx4Args& a) {
   return (int)hipGetLastError();
 }
 
+// The block's tile, rows x tokens, by what the fullest CU takes: `first` for the
+// call, and for each of its tiles `end` and `step` for 128 columns, in ns.
+// Measured, us, where two tiles part (weights in the caches):
+//   4096 x 4096: 32 tokens 16x32 3.4, 32x32 3.7; 64 tokens 16x32 4.3, 32x32 3.9;
+//   128 tokens 32x64 5.1, 32x32 5.3, 64x64 6.3; 256 tokens 64x64 6.6, 32x64 7.1;
+//   512 tokens 64x64 9.0, 64x128 9.0, 128x128 11.7; 1024 tokens 64x128 12.8,
+//   128x128 12.5; 4096 tokens 128x128 33.7, 256x256 34.5, 64x128 40.2
+//   4096 x 11008: 128 tokens 32x64 9.1, 64x64 11.4; 8192 tokens 128x128 150.8,
+//   256x256 138.6; 11008 x 4096: 64 tokens 64x64 6.5, 32x64 7.5; 8192 tokens
+//   128x128 163.9, 256x256 170.6; 32000 x 4096, 8192 tokens 480.8 and 427.9
 int launch_mx4q(const Mx4Args& a) {
-  if (a.T <= 16) go<1, 1, true>(a);
-  else go<4, 2, true>(a);
+  constexpr struct {
+    int rows, toks, first, end, step;
+  } kTiles[] = {{16, 16, 2200, 0, 32}, {16, 32, 2300, 0, 35},    {32, 32, 2100, 0, 48},      {32, 64, 2600, 0, 70},
+                {64, 64, 3200, 0, 92}, {64, 128, 3400, 0, 148}, {128, 128, 2000, 1600, 200}, {256, 256, 2000, 5000, 770}};
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int c = 0; c < 8; ++c) {
+    const int64_t tiles = (int64_t)((a.out + kTiles[c].rows - 1) / kTiles[c].rows) * ((a.T + kTiles[c].toks - 1) / kTiles[c].toks);
+    const int64_t cost = kTiles[c].first + (tiles + 255) / 256 * (kTiles[c].end + (int64_t)kTiles[c].step * (a.in / 128));
+    if (cost < least) least = cost, best = c;
+  }
+  switch (best) {
+    case 0: go<1, 1, true>(a); break;
+    case 1: go<1, 2, true>(a); break;
+    case 2: go<2, 2, true>(a); break;
+    case 3: go<2, 4, true>(a); break;
+    default: return launch_mx4_tiles(a, best - 4);
+  }
   return (int)hipGetLastError();
 }
 

@@ -651,6 +651,39 @@ def test_apply_mx4q(t_, out, inn):
     assert np.array_equal(host_bits(y)[:t_], first[:t_])
 
 
+# Every tile of the product (by the rule in launch_mx4q): one or several for a block, columns of 1, 2, 3 and 0 more
+# than whole groups of 512, and fewer than 512; rows and tokens that end inside a tile.
+@pytest.mark.parametrize("t_,out,inn", [
+    (32, 4096, 4096), (17, 4224, 3968),                                              # 16 x 32
+    (100, 6400, 1536), (300, 6400, 640), (100, 6400, 1280), (700, 8064, 256), (3000, 1152, 384),   # 32 x 64
+    (390, 4224, 1024), (520, 8064, 640), (520, 8064, 768), (520, 8064, 896), (4100, 3200, 128),    # 64 x 64
+    (1500, 4224, 512), (1500, 4224, 640), (1500, 4224, 768), (390, 4096, 896), (1100, 6400, 256),  # 64 x 128
+    (2600, 4096, 1536), (2600, 4096, 1664), (390, 6400, 768), (520, 4096, 896), (900, 4096, 384),  # 128 x 128
+    (5000, 6400, 1536), (2000, 8064, 1152), (5000, 6400, 1792), (5000, 6528, 1408)])               # 256 x 256
+def test_apply_mx4q_tiles(t_, out, inn):
+    t = torch()
+    note("mx4q tiles", t_, out, inn)
+    rng = np.random.default_rng(t_ + out + inn)
+    w, view = mx4_case(rng, out, inn)
+    x = vals(bits(rng.normal(size=(t_, inn)).astype(np.float32)))
+    xq = mx4_empty(t_, inn)
+    trs.dc_mx4_pack_device(dev_bits(bits(x)), xq)
+    x4 = t.from_numpy(step.mx4_matrix(*step.mx4_quantize(x))).cuda()
+    wd = t.from_numpy(w).cuda()
+    y = t.full((t_ + 1, out), float("nan"), dtype=t.bfloat16, device="cuda")
+    trs.dc_apply_mx4q(view, xq, y[:t_])
+    t.cuda.synchronize()
+    first = y.clone()
+    want = x4 @ wd.t().contiguous()
+    tol = BF16 * want.abs() + (inn * 1.125 + 8) * 2.0 ** -23 * (x4.abs() @ wd.abs().t().contiguous())
+    err = (y[:t_].double() - want).abs()
+    assert bool((err <= tol).all()) and float(err.norm() / want.norm()) <= BF16
+    assert bool(y[t_:].isnan().all())
+    y.zero_()
+    trs.dc_apply_mx4q(view, xq, y[:t_])
+    assert t.equal(y[:t_], first[:t_])
+
+
 @pytest.mark.parametrize("t_", [1, 20, 70, 300])
 def test_mx4_values_that_are_not_finite(t_):
     """A NaN block reaches its row, an x that is not finite its token; neither reaches further."""
