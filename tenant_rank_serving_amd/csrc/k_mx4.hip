@@ -13,32 +13,17 @@
 namespace dc {
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
+#include "mx4_common.h"
+
 constexpr int kFp4 = 4;   // the matrix core's format number
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
-}
-
-// The scale byte as the fp32 number whose exponent field it is: the conversions
-// read that field (0: 2^-127), and 255 has to be NaN, not infinity.
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return __uint_as_float(byte == 255 ? 0x7FC00000u : byte << 23);
-}
-
-// 8 codes as bf16.
-__device__ __forceinline__ bf16x8 codes8(uint32_t w, float s) {
-  uint4 r;
-  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-  return __builtin_bit_cast(bf16x8, r);
 }
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -103,29 +88,34 @@ __global__ void __launch_bounds__(256) k_mx4_pack(const uint16_t* __restrict__ X
 
 __global__ void k_mx4_flag(uint32_t* flag) { *flag = 0; }
 
-// The same tiles the other way.
+// The same tiles the other way.  Lane l takes 8 codes of row l/4 at a time, so
+// that 4 lanes write a block's 64 bytes side by side (a lane's whole block is 64
+// bytes in 4 stores, each of 16 bytes of as many cache lines: 40 us for 4096 x 14336
+// where this takes 24).
 __global__ void __launch_bounds__(256) k_mx4_dequant(const uint8_t* __restrict__ w, uint16_t* __restrict__ X, int64_t stride,
                                                      int rows, int cols) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int gc = cols / 128, hc = (gc + 3) / 4;
   const int T = blockIdx.x / hc * 4 + wave, H = blockIdx.x % hc;
   if (T * 16 >= rows) return;
-  const int row = T * 16 + (lane & 15);
-  const size_t codes = (size_t)((rows + 15) / 16) * gc * 1024;
-  const uint32_t scales = *reinterpret_cast<const uint32_t*>(w + codes + ((size_t)T * hc + H) * 256 + lane * 4);
-  uint16_t* dst = X + (int64_t)row * stride + 512 * H + 32 * (lane >> 4);
+  const int i = lane >> 2, e = lane & 3, row = T * 16 + i;
+  const uint8_t* code = w + ((size_t)T * gc + 4 * H) * 1024 + i * 16 + e * 4;
+  const uint8_t* scale = w + (size_t)((rows + 15) / 16) * gc * 1024 + ((size_t)T * hc + H) * 256 + i * 4;
+  const int n = min(4, gc - 4 * H);
+  uint32_t s[4], c[4][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (4 * H + j >= gc) break;
-    const uint4 c = *reinterpret_cast<const uint4*>(w + ((size_t)T * gc + 4 * H + j) * 1024 + lane * 16);
-    const float s = scale_of(scales >> (8 * j) & 255u);
-    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
-    if (row < rows) {
+  for (int q = 0; q < 4; ++q) {
+    s[q] = *reinterpret_cast<const uint32_t*>(scale + q * 64);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(dst + 128 * j + 8 * i) = __builtin_bit_cast(uint4, codes8(u[i], s));
-    }
+    for (int j = 0; j < 4; ++j) c[j][q] = *reinterpret_cast<const uint32_t*>(code + min(j, n - 1) * 1024 + q * 256);
   }
+  if (row >= rows) return;
+  uint16_t* dst = X + (int64_t)row * stride + 512 * H + 8 * e;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (j < n) *reinterpret_cast<uint4*>(dst + 128 * j + 32 * q) = __builtin_bit_cast(uint4, codes8(c[j][q], scale_of(s[q] >> (8 * j) & 255u)));
 }
 
 // ---------------------------------------------------------------- products
@@ -217,9 +207,25 @@ void go(const Mx4Args& a) {
 
 }  // namespace
 
+// Up to 16 tokens: row tiles a block, by the accesses of the fullest CU's L1 (17 for
+// a row tile, 4 for a token's x) and the rounds of 256 blocks.  us, 1 / 7 / 16
+// tokens: 4096 x 4096 16 rows 3.4 / 4.4 / 5.9, 48 rows 4.7 / 5.3 / 6.8; 11008 x 4096
+// 16 rows 5.7 / 8.9 / 13.4, 48 rows 4.8 / 5.5 / 7.2; 32000 x 4096 32 rows 11.9 / 12.7
+// / 18.6, 64 rows 13.1 / 13.3 / 15.5.
 int launch_mx4(const Mx4Args& a) {
-  if (a.T <= 16) go<1, 1, false>(a);
-  else go<4, 2, false>(a);
+  if (a.T > 16) return launch_mx4_few(a);
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int rt = 1; rt <= 4; ++rt) {
+    const int64_t cost = ((a.out / 16 + rt - 1) / rt + 255) / 256 * (17 * rt + 4 * a.T);
+    if (cost < least) least = cost, best = rt;
+  }
+  switch (best) {
+    case 1: go<1, 1, false>(a); break;
+    case 2: go<2, 1, false>(a); break;
+    case 3: go<3, 1, false>(a); break;
+    default: go<4, 1, false>(a); break;
+  }
   return (int)hipGetLastError();
 }
 

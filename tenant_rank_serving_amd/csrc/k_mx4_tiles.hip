@@ -22,34 +22,14 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+#include "mx4_common.h"
 
 constexpr int kFp4 = 4;
 constexpr int NS = 4;   // tiles in LDS: as many as steps that share a scale word
 
 __device__ __forceinline__ v8i piece(u32x4 w) { return v8i{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0}; }
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  bf16x2 v;
-  v[0] = (__bf16)a;
-  v[1] = (__bf16)b;
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-// 16 (4) bytes a lane from base + voff to lds + 16 (4) lane.
-__device__ __forceinline__ void to_lds16(const uint8_t* base, int voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-__device__ __forceinline__ void to_lds4(const uint8_t* base, int voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
-}
-
-// At most N of the wave's loads still on their way; its LDS reads are done, and
-// so are every other wave's.
-template <int N>
-__device__ __forceinline__ void wait_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
 
 template <int TA, int TB>
 struct TilesLds {
@@ -61,7 +41,7 @@ struct TilesLds {
   alignas(256) uint8_t bs[TB * kBs];
 };
 
-// The same, or as many loads as there are where `fresh`.  (The branch is hidden
+// wait_barrier, or as many loads as there are where `fresh`.  (The branch is hidden
 // from the compiler, which makes copies of the steps for either side.)
 template <int N>
 __device__ __forceinline__ void wait_barrier_unless(int fresh) {

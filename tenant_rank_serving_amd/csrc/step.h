@@ -76,6 +76,7 @@ struct Mx4Args {
 // Bytes of the codes of a matrix.
 inline size_t mx4_codes(int32_t rows, int32_t cols) { return (size_t)((rows + 15) / 16) * 16 * (size_t)cols / 2; }
 int launch_mx4(const Mx4Args& a);
+int launch_mx4_few(const Mx4Args& a);   // of it, more than 16 tokens
 int launch_mx4q(const Mx4Args& a);
 int launch_mx4_tiles(const Mx4Args& a, int32_t size);   // of it, by tiles in LDS: 64 x 64, 64 x 128, 128 x 128, 256 x 256
 int launch_mx4_pack(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, uint8_t* dst, uint32_t* flag,

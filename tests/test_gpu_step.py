@@ -651,6 +651,33 @@ def test_apply_mx4q(t_, out, inn):
     assert np.array_equal(host_bits(y)[:t_], first[:t_])
 
 
+# Every tile of the products with bf16 activations (by the rules in launch_mx4 and launch_mx4_few).
+@pytest.mark.parametrize("t_,out,inn", [
+    (1, 4096, 512), (7, 11008, 640), (16, 8320, 384), (2, 32000, 256), (13, 12416, 896), (3, 8192, 256),   # 16 to 64 rows, up to 16 tokens
+    (32, 4096, 1152), (17, 128, 2176), (64, 4096, 1280), (50, 4224, 640), (100, 4096, 896),       # 32 x 16, 32 x 32
+    (20, 11008, 1152), (128, 4224, 1408), (64, 11008, 640), (250, 4096, 384), (60, 32000, 128),   # 64 x 32 of 8 and of 4 waves
+    (500, 4096, 1152), (130, 11008, 512), (700, 8064, 640), (64, 32000, 1664)])                   # 128 x 64
+def test_apply_mx4_tiles(t_, out, inn):
+    t = torch()
+    note("mx4 tiles", t_, out, inn)
+    rng = np.random.default_rng(t_ + out + inn)
+    w, view = mx4_case(rng, out, inn)
+    xd = dev_bits(bits(rng.normal(size=(t_, inn)).astype(np.float32)))
+    wd = t.from_numpy(w).cuda()
+    y = t.full((t_ + 1, out), float("nan"), dtype=t.bfloat16, device="cuda")
+    trs.dc_apply_mx4(view, xd, y[:t_])
+    t.cuda.synchronize()
+    first = y.clone()
+    want = xd.double() @ wd.t().contiguous()
+    tol = BF16 * want.abs() + (inn * 1.125 + 8) * 2.0 ** -23 * (xd.double().abs() @ wd.abs().t().contiguous())
+    err = (y[:t_].double() - want).abs()
+    assert bool((err <= tol).all()) and float(err.norm() / want.norm()) <= BF16
+    assert bool(y[t_:].isnan().all())
+    y.zero_()
+    trs.dc_apply_mx4(view, xd, y[:t_])
+    assert t.equal(y[:t_], first[:t_])
+
+
 # Every tile of the product (by the rule in launch_mx4q): one or several for a block, columns of 1, 2, 3 and 0 more
 # than whole groups of 512, and fewer than 512; rows and tokens that end inside a tile.
 @pytest.mark.parametrize("t_,out,inn", [
