@@ -919,7 +919,7 @@ dc_status dc_kv_copy(const dc_kv_cache* layers, int32_t n_layers, const int32_t*
  *             sequence's positions must ascend, and its pages be held by it
  *             alone (as far as they are written)
  * Positions and pages out of range are left out.  Errors as for dc_kv_copy
- * (2^24 blocks of 64 tokens and 16 heads, or of a sequence in place).
+ * (2^24 blocks of 64 tokens and 4 heads, or of a sequence in place).
  */
 dc_status dc_kv_compact(const dc_kv_cache* layers, int32_t n_layers, const int32_t* from, int32_t seqs, int32_t width,
                         const int32_t* keep_start, const int32_t* keep, int32_t n, const int32_t* to, void* stream);

@@ -12,6 +12,8 @@
 namespace dc {
 namespace {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 // ------------------------------------------------------------------ tables
 constexpr int kResizeThreads = 1024, kWaves = kResizeThreads / 64;
 
@@ -265,19 +267,20 @@ __device__ __forceinline__ int64_t token_at(const LayerArgs& a, const int32_t* t
   return p * a.page_stride + (pos & ((1 << a.shift) - 1)) * a.slot_stride;
 }
 
-// Block: 64 kept tokens, 16 heads of one layer's keys or values.  To other
-// pages the blocks are independent (`tiles` of them); in place one block moves
-// a sequence's tokens, 64 at a time: sources ascend and lie at or behind their
-// places, so a tile's places hold nothing that is still to be read once the
-// tile itself has been.
+// Block: 64 kept tokens of 64 >> a.pieces heads of one layer's keys or values, 16
+// pieces of 16 bytes a thread.  To other pages the blocks are independent.  In
+// place one block moves a sequence's tokens, a tile after the other: sources
+// ascend and lie at or behind their places, so a tile's places hold nothing that
+// is still to be read once the tile itself has been.  The next tile's places are
+// looked up while this one's pieces are on their way.
 template <bool InPlace>
 __global__ void __launch_bounds__(256) k_compact(LayerArgs a, const int32_t* from, const int32_t* to,
                                                  const int32_t* start, const int32_t* keep, int seqs, int width, int n) {
-  __shared__ int64_t src[kCompactTokens], dst[kCompactTokens];
+  constexpr int kHalves = InPlace ? 2 : 1, kUnits = 16;
+  __shared__ int64_t src[kHalves][kCompactTokens], dst[kHalves][kCompactTokens];
   const int tid = threadIdx.x;
   uint8_t* pool = pool_of(a, blockIdx.y);
-  const int h0 = blockIdx.z * kCompactHeads, heads = min(kCompactHeads, a.heads - h0);
-  const int log_units = 6 + a.pieces;   // of a head's tile
+  const int log_heads = 6 - a.pieces, h0 = blockIdx.z << log_heads, heads = min(1 << log_heads, a.heads - h0);
   int t0, t1, seq0 = 0;
   if constexpr (InPlace) {
     seq0 = blockIdx.x;
@@ -287,50 +290,60 @@ __global__ void __launch_bounds__(256) k_compact(LayerArgs a, const int32_t* fro
     t0 = blockIdx.x * kCompactTokens;
     t1 = min(t0 + kCompactTokens, n);
   }
+  if (t0 >= t1) return;
+  auto look_up = [&](int tile, int half) {
+    if (tid >= kCompactTokens) return;
+    const int j = tile + tid;
+    int64_t s = -1, d = -1;
+    if (j < t1) {
+      const int at = keep[j];
+      int seq = seq0;
+      if constexpr (!InPlace) {   // the last sequence that starts at or before j
+        int lo = 0, hi = seqs;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (start[mid] <= j) lo = mid + 1; else hi = mid;
+        }
+        seq = lo - 1;
+      }
+      if (seq >= 0 && j < start[seq + 1]) {
+        s = token_at(a, from, width, seq, at);
+        d = token_at(a, InPlace ? from : to, width, seq, j - max(start[seq], 0));
+      }
+    }
+    src[half][tid] = s != d && d >= 0 ? s : -1;   // (in place: where it is already)
+    dst[half][tid] = d;
+  };
+  // the thread's pieces: consecutive threads take a row's, then the next token's
+  const int c = tid & ((1 << a.pieces) - 1), tok0 = tid >> a.pieces, log_step = 8 - a.pieces;
+  auto piece_of = [&](int i, int* tok, int* h) {
+    const int u = tok0 + (i << log_step);
+    *tok = u & (kCompactTokens - 1);
+    *h = u >> 6;
+  };
+  look_up(t0, 0);
+  __syncthreads();
+  int half = 0;
   for (int tile = t0; tile < t1; tile += kCompactTokens) {
-    if (tid < kCompactTokens) {
-      const int j = tile + tid;
-      int64_t s = -1, d = -1;
-      if (j < t1) {
-        int seq = seq0;
-        if constexpr (!InPlace) {   // the last sequence that starts at or before j
-          int lo = 0, hi = seqs;
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (start[mid] <= j) lo = mid + 1; else hi = mid;
-          }
-          seq = lo - 1;
-        }
-        if (seq >= 0 && j < start[seq + 1]) {
-          s = token_at(a, from, width, seq, keep[j]);
-          d = token_at(a, InPlace ? from : to, width, seq, j - max(start[seq], 0));
-        }
-      }
-      src[tid] = s != d && d >= 0 ? s : -1;   // (in place: where it is already)
-      dst[tid] = d;
-    }
-    __syncthreads();
-    constexpr int kUnits = 16;   // a thread's pieces at a time
-    for (int u0 = 0; u0 < (heads << log_units); u0 += 256 * kUnits) {
-      uint4 x[kUnits];
+    u32x4 x[kUnits];
+    int64_t d[kUnits];
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + 256 * i + tid, h = u >> log_units, tok = (u >> a.pieces) & (kCompactTokens - 1);
-        if (h >= heads || src[tok] < 0) continue;
-        x[i] = *reinterpret_cast<const uint4*>(pool + src[tok] + (h0 + h) * a.head_stride + 16 * (u & ((1 << a.pieces) - 1)));
-      }
-      if constexpr (InPlace) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();   // every piece of these heads' tile has been read
-      }
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int u = u0 + 256 * i + tid, h = u >> log_units, tok = (u >> a.pieces) & (kCompactTokens - 1);
-        if (h >= heads || src[tok] < 0) continue;
-        *reinterpret_cast<uint4*>(pool + dst[tok] + (h0 + h) * a.head_stride + 16 * (u & ((1 << a.pieces) - 1))) = x[i];
-      }
+    for (int i = 0; i < kUnits; ++i) {
+      int tok, h;
+      piece_of(i, &tok, &h);
+      const int64_t s = src[half][tok], more = (h0 + h) * a.head_stride + 16 * c;
+      d[i] = h < heads && s >= 0 ? dst[half][tok] + more : -1;
+      if (d[i] >= 0) x[i] = *reinterpret_cast<const u32x4*>(pool + s + more);
     }
-    __syncthreads();
+    if constexpr (InPlace) {
+      if (tile + kCompactTokens < t1) look_up(tile + kCompactTokens, half ^ 1);
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();   // every piece of the tile has been read
+      half ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      if (d[i] >= 0) *reinterpret_cast<u32x4*>(pool + d[i]) = x[i];
   }
 }
 
@@ -355,7 +368,7 @@ int launch_copy(const LayerArgs& a, const int32_t* copies, int32_t n, void* stre
 
 int launch_compact(const LayerArgs& a, const int32_t* from, const int32_t* to, const int32_t* start,
                    const int32_t* keep, int32_t seqs, int32_t width, int32_t n, void* stream) {
-  const unsigned groups = (unsigned)((a.heads + kCompactHeads - 1) / kCompactHeads);
+  const unsigned per = 64u >> a.pieces, groups = ((unsigned)a.heads + per - 1) / per;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (to)
     hipLaunchKernelGGL(k_compact<false>, dim3((unsigned)((n + kCompactTokens - 1) / kCompactTokens), 2u * (unsigned)a.layers, groups),

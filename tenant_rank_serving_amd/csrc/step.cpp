@@ -223,7 +223,7 @@ dc_status dc_kv_compact(const dc_kv_cache* layers, int32_t n_layers, const int32
   if (st != DC_OK) return st;
   if (n < 0 || seqs < 0 || width < 0) return DC_ERR_INVALID_ARG;
   if (width > (INT32_MAX >> a.shift)) return DC_ERR_SHAPE;
-  const int64_t groups = ((int64_t)a.heads + kCompactHeads - 1) / kCompactHeads;
+  const int64_t groups = ((int64_t)a.heads + 3) / 4;   // (64 >> pieces heads a block, 4 at least)
   const int64_t tiles = std::max<int64_t>(((int64_t)n + kCompactTokens - 1) / kCompactTokens, seqs);
   if (groups > 65535 || !mul_fits(2 * (int64_t)n_layers * groups, tiles, kMostBlocks)) return DC_ERR_UNSUPPORTED;
   if (n == 0 || seqs == 0 || width == 0) return DC_OK;

@@ -58,9 +58,8 @@ struct LayerArgs {
   int32_t pieces;                                  // log2 of the 16-byte pieces of a head's row
 };
 int launch_copy(const LayerArgs& a, const int32_t* copies, int32_t n, void* stream);
-// 16-byte pieces that a block of the copy, and of compaction, moves.
-constexpr int kCopyBlock = 1024;
-constexpr int kCompactTokens = 64, kCompactHeads = 16;
+constexpr int kCopyBlock = 1024;                    // 16-byte pieces that a block of the copy moves
+constexpr int kCompactTokens = 64;                  // tokens of a block of compaction; 64 >> pieces heads
 int launch_compact(const LayerArgs& a, const int32_t* from, const int32_t* to, const int32_t* start,
                    const int32_t* keep, int32_t seqs, int32_t width, int32_t n, void* stream);
 
