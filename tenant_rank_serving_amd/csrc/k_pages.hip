@@ -230,8 +230,11 @@ __device__ __forceinline__ uint8_t* pool_of(const LayerArgs& a, int lv) {
   return lv & 1 ? a.v[lv >> 1] : a.k[lv >> 1];
 }
 
-// Piece u of a page, in the order of memory: rows of a head, or heads of a row.
+// Piece u of a page, in the order of memory: rows of a head, or heads of a row
+// (Whole: a page without gaps).
+template <bool Whole>
 __device__ __forceinline__ int64_t piece_at(const LayerArgs& a, int u) {
+  if constexpr (Whole) return 16 * (int64_t)u;
   const int c = u & ((1 << a.pieces) - 1), r = u >> a.pieces;
   int h, s;
   if (a.slot_stride <= a.head_stride) h = r >> a.shift, s = r & ((1 << a.shift) - 1);
@@ -240,21 +243,24 @@ __device__ __forceinline__ int64_t piece_at(const LayerArgs& a, int u) {
 }
 
 // Block: 16 KiB of a page of one layer's keys or values.
+template <bool Whole>
 __global__ void __launch_bounds__(256) k_copy(LayerArgs a, const int32_t* copies) {
   const int64_t from = copies[2 * blockIdx.x], to = copies[2 * blockIdx.x + 1];
   if (from < 0 || from >= a.num_pages || to < 0 || to >= a.num_pages || from == to) return;
   uint8_t* pool = pool_of(a, blockIdx.y);
+  const uint8_t* src = pool + from * a.page_stride;
+  uint8_t* dst = pool + to * a.page_stride;
   const int pieces = a.heads << (a.shift + a.pieces), u0 = blockIdx.z * kCopyBlock + threadIdx.x;
-  uint4 x[kCopyBlock / 256];
+  u32x4 x[kCopyBlock / 256];
 #pragma unroll
   for (int i = 0; i < kCopyBlock / 256; ++i) {
     const int u = u0 + 256 * i;
-    if (u < pieces) x[i] = *reinterpret_cast<const uint4*>(pool + from * a.page_stride + piece_at(a, u));
+    if (u < pieces) x[i] = *reinterpret_cast<const u32x4*>(src + piece_at<Whole>(a, u));
   }
 #pragma unroll
   for (int i = 0; i < kCopyBlock / 256; ++i) {
     const int u = u0 + 256 * i;
-    if (u < pieces) *reinterpret_cast<uint4*>(pool + to * a.page_stride + piece_at(a, u)) = x[i];
+    if (u < pieces) *reinterpret_cast<u32x4*>(dst + piece_at<Whole>(a, u)) = x[i];
   }
 }
 
@@ -361,8 +367,13 @@ int launch_fork(const TableArgs& t, const int32_t* src, const int32_t* dst, int3
 
 int launch_copy(const LayerArgs& a, const int32_t* copies, int32_t n, void* stream) {
   const unsigned parts = (unsigned)(((a.heads << (a.shift + a.pieces)) + kCopyBlock - 1) / kCopyBlock);
-  hipLaunchKernelGGL(k_copy, dim3((unsigned)n, 2u * (unsigned)a.layers, parts), dim3(256), 0,
-                     reinterpret_cast<hipStream_t>(stream), a, copies);
+  const int64_t row = INT64_C(16) << a.pieces, inner = a.slot_stride <= a.head_stride ? a.slot_stride : a.head_stride;
+  const int64_t outer = a.slot_stride <= a.head_stride ? a.head_stride : a.slot_stride;
+  const int64_t count = a.slot_stride <= a.head_stride ? INT64_C(1) << a.shift : a.heads;
+  const dim3 g((unsigned)n, 2u * (unsigned)a.layers, parts);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (inner == row && outer == count * row) hipLaunchKernelGGL(k_copy<true>, g, dim3(256), 0, st, a, copies);
+  else hipLaunchKernelGGL(k_copy<false>, g, dim3(256), 0, st, a, copies);
   return (int)hipGetLastError();
 }
 
