@@ -25,21 +25,29 @@ namespace {
 constexpr int kThreads = kVerifyThreads, kVec = kVerifyVec;
 constexpr float kMinusInf = -__builtin_inff();
 
+// s f + c with the constant in scalar registers: left to itself the compiler takes
+// the accumulating form and moves each constant to vector registers first, two
+// moves a step.
+__device__ __forceinline__ double fma_c(double s, double f, double c) {
+  double r;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(s), "v"(f), "s"(c));
+  return r;
+}
+
 // 2^y for y <= 0 (a little above, too); 0 for -infinity and for NaN.
 __device__ __forceinline__ double exp2_neg(double y) {
-  y = fmax(y, -1100.0);
-  const double n = rint(y), f = y - n;   // |f| <= 1/2
+  y = __builtin_fmax(y, -1100.0);
+  const double n = __builtin_rint(y), f = y - n;   // |f| <= 1/2
   // interpolates 2^f at the zeros of the Chebyshev polynomial of degree 10
-  double s = 1.0205905320493103e-07;
-  s = __builtin_fma(s, f, 1.3259645243929057e-06);
-  s = __builtin_fma(s, f, 1.5252672925346873e-05);
-  s = __builtin_fma(s, f, 0.00015403433751254997);
-  s = __builtin_fma(s, f, 0.0013333558200793719);
-  s = __builtin_fma(s, f, 0.009618129193934304);
-  s = __builtin_fma(s, f, 0.05550410866465168);
-  s = __builtin_fma(s, f, 0.2402265069564034);
-  s = __builtin_fma(s, f, 0.6931471805599462);
-  s = __builtin_fma(s, f, 1.0000000000000135);
+  double s = fma_c(f, 1.0205905320493103e-07, 1.3259645243929057e-06);
+  s = fma_c(s, f, 1.5252672925346873e-05);
+  s = fma_c(s, f, 0.00015403433751254997);
+  s = fma_c(s, f, 0.0013333558200793719);
+  s = fma_c(s, f, 0.009618129193934304);
+  s = fma_c(s, f, 0.05550410866465168);
+  s = fma_c(s, f, 0.2402265069564034);
+  s = fma_c(s, f, 0.6931471805599462);
+  s = fma_c(s, f, 1.0000000000000135);
   return __builtin_ldexp(s, (int)n);
 }
 
@@ -148,16 +156,24 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(VerifyArgs a) {
   const int v0 = c * U * kThreads + tid;
 #pragma unroll
   for (int u = 0; u < U; ++u) load8<F32>(l, (v0 + u * kThreads) * kVec - lead, V, v[u]);
+  // the largest logit; where it first is, for greedy rows alone
   float m = kMinusInf;
   int at = 0x7FFFFFFF;
   bool nan = false;
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      nan |= v[u][j] != v[u][j];
-      if (v[u][j] > m) m = v[u][j], at = (v0 + u * kThreads) * kVec - lead + j;
+    for (int j = 0; j < kVec; j += 2) {
+      nan |= __builtin_isunordered(v[u][j], v[u][j + 1]);
+      m = fmaxf(fmaxf(m, v[u][j]), v[u][j + 1]);
     }
+  if (k == 0.0) {
+#pragma unroll
+    for (int u = U - 1; u >= 0; --u)
+#pragma unroll
+      for (int j = kVec - 1; j >= 0; --j)
+        if (v[u][j] == m) at = (v0 + u * kThreads) * kVec - lead + j;
+  }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) {
     const float m2 = __shfl_xor(m, x);
