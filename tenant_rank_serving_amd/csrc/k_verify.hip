@@ -3,11 +3,9 @@
 // the new token is drawn from max(p - q, 0), behind the last one from p.
 //
 // Two launches.  k_verify_stats: for every row its largest logit and the sum of
-// the exponentials, a block for each piece of a row.  k_verify_pick: a block for
-// each piece of a sequence's last row; every block joins the rows' sums and
-// comes to the same decision, then sums its piece's weights max(p - q, 0), and
-// the block that arrives last looks for the piece, the vector and the token
-// that r sum_k w_k falls on.
+// the exponentials, a block for each piece of a row.  k_verify_pick: joins the
+// rows' sums, decides, and looks for the piece, the vector and the token that
+// r sum_k w_k falls on.
 //
 // The answers are whole numbers: a token changes when rounding moves one of V
 // borders past r, which with sums good to d happens 2 V d times of all (V = 10^5
@@ -34,7 +32,9 @@ __device__ __forceinline__ double fma_c(double s, double f, double c) {
   return r;
 }
 
-// 2^y for y <= 0 (a little above, too); 0 for -infinity and for NaN.
+// 2^y for y <= 0 (a little above, too); 0 for -infinity and for NaN.  (The whole
+// part by additions of 1.5 2^52 and an integer addition to the exponent instead of
+// rint and ldexp: no faster.)
 __device__ __forceinline__ double exp2_neg(double y) {
   y = __builtin_fmax(y, -1100.0);
   const double n = __builtin_rint(y), f = y - n;   // |f| <= 1/2
@@ -119,8 +119,10 @@ __device__ __forceinline__ void keep_larger(float& m, int& at, float m2, int at2
 }
 
 // ------------------------------------------------------------------ stats
-// Block (piece, row, side).  Reads are bound by HBM where there are many; the 17
-// fp64 operations of an exponential keep the vector unit busy for about as long.
+// Block (piece, row, side).  Bound by the vector unit, whose 28 instructions for a
+// logit are 18 fp64 ones of the exponential, its conversion, the maximum and the
+// test for NaN, and for fp32 logits by HBM almost as much: 455 rows of 100003 fp32
+// logits 43 us (4.2 TB/s), 829 rows of bf16 67 us (2.5 TB/s).
 template <bool F32, int U>
 __global__ void __launch_bounds__(kThreads) k_verify_stats(VerifyArgs a) {
   __shared__ float sm[4];
@@ -241,30 +243,42 @@ struct Judged {
   float share;       // p(token)
 };
 
-// The weights of a vector's logits: p - q where that is positive, and p.
-template <bool F32>
-__device__ __forceinline__ void weights8(const float* lp, const float* lq, const RowStat& p, const RowStat& q, double k,
-                                         int i0, int less, bool minus, double* w, double* sp) {
-  const double ip = 1.0 / p.z, iq = minus ? 1.0 / q.z : 0.0;
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ double scan64(double v, int lane) {
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    const double pj = weight(lp[j], p.m, k) * ip;
-    double qj = 0.0;
-    if (minus) qj = weight(lq[j], q.m, k) * iq;
-    if (i0 + j == less) qj = 1.0;
-    sp[j] = pj;
-    w[j] = fmax(pj - qj, 0.0);
+  for (int x = 1; x < 64; x <<= 1) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t o = (uint64_t)__shfl_up((uint32_t)(b >> 32), x) << 32 | __shfl_up((uint32_t)b, x);
+    if (lane >= x) v += __builtin_bit_cast(double, o);
   }
+  return v;
+}
+__device__ __forceinline__ double lane64(double v, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)__shfl((uint32_t)(b >> 32), l) << 32 | __shfl((uint32_t)b, l));
 }
 
-template <bool F32, int U>
-__global__ void __launch_bounds__(kThreads) k_verify_pick(VerifyArgs a) {
+// A thread for each vector of a piece.  With a draft model's logits (Q) every
+// piece has its block and the last one to finish chooses.  Without them the
+// pieces' sums are those of the statistics, but for the piece that holds the
+// token taken off, and one block does it all (64 sequences of 100003 fp32 logits
+// 42 -> 16.5 us).
+//
+// Bound by latency (decision, sums, search and the piece's own exponentials wait
+// for each other) and with many blocks by the vector unit, half of it for the
+// decision that each block repeats: 63 sequences of 9 rows of 100003 bf16 logits
+// take 35 us by pieces of 2048 logits, 29 by 4096, 44 by 8192 (blocks of 16 waves
+// leave CUs waiting for their slowest).
+template <bool F32, bool Q, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_verify_pick(VerifyArgs a) {
+  constexpr int WAVES = THREADS / 64;
   __shared__ Judged judged[16];
-  __shared__ double sr[U * 4], sp[U * 4];
-  __shared__ int last_flag, found[2];
+  __shared__ double sr[WAVES], sp[WAVES];
+  __shared__ int last_flag, found[2], first_of[WAVES], last_of[WAVES];
   __shared__ double left_of[1];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int c = blockIdx.x % a.chunks, seq = blockIdx.x / a.chunks, V = a.vocab;
+  const int pieces = Q ? a.pieces : a.chunks, blocks = Q ? pieces : 1;   // blocks of a sequence
+  const int c = blockIdx.x % blocks, seq = blockIdx.x / blocks, V = a.vocab;
   const int lo = min(max(a.q_start[seq], 0), a.n), hi = min(max(a.q_start[seq + 1], lo), a.n);
   if (lo == hi) {
     if (c == 0 && tid == 0) a.count[seq] = 0;
@@ -274,51 +288,59 @@ __global__ void __launch_bounds__(kThreads) k_verify_pick(VerifyArgs a) {
   const bool greedy = k == 0.0;
 
   // rows lo, lo + 1, .. 16 at a time, 16 lanes each, until a draft falls
-  int stop = -1;
+  int stop = -1, base = lo;
   Judged end{};
   for (int r0 = lo; stop < 0; r0 += 16) {
     const int row = min(r0 + (tid >> 4), hi - 1);
-    const bool drafted = row + 1 < hi;
     Judged g{};
-    g.token = drafted ? a.tokens[row + 1] : -1;
-    const bool inside = g.token >= 0 && g.token < V;
-    float lp = kMinusInf, lq = kMinusInf;
-    if (inside) lp = logit<F32>(row_of<F32>(a.p, a.ps, row), g.token);
-    if (inside && a.q) lq = logit<F32>(row_of<F32>(a.q, a.qs, row), g.token);
-    g.p = join16(a.part + (size_t)row * 2 * a.chunks, a.chunks, k);
-    if (a.q && drafted && !greedy) g.q = join16(a.part + ((size_t)row * 2 + 1) * a.chunks, a.chunks, k);
-    if (inside && g.p.z > 0.0) {
-      if (greedy) {
-        g.stands = g.token == g.p.at;
-        g.share = 1.f;
-      } else {
-        const double pt = weight(lp, g.p.m, k) / g.p.z;
-        g.share = (float)pt;
-        // NaN sums (no distribution) compare false
-        const double qt = a.q ? (g.q.z > 0.0 ? weight(lq, g.q.m, k) / g.q.z : __builtin_nan("")) : 1.0;
-        g.stands = (double)a.accept[row] * qt < pt;
+    if (tid < 256 && r0 + wave * 4 < hi) {
+      const bool drafted = row + 1 < hi;
+      g.token = drafted ? a.tokens[row + 1] : -1;
+      const bool inside = g.token >= 0 && g.token < V;
+      float lp = kMinusInf, lq = kMinusInf;
+      if (inside) lp = logit<F32>(row_of<F32>(a.p, a.ps, row), g.token);
+      if (Q && inside) lq = logit<F32>(row_of<F32>(a.q, a.qs, row), g.token);
+      g.p = join16(a.part + (size_t)row * 2 * a.chunks, a.chunks, k);
+      if (Q && drafted && !greedy) g.q = join16(a.part + ((size_t)row * 2 + 1) * a.chunks, a.chunks, k);
+      if (inside && g.p.z > 0.0) {
+        if (greedy) {
+          g.stands = g.token == g.p.at;
+          g.share = 1.f;
+        } else {
+          const double pt = weight(lp, g.p.m, k) / g.p.z;
+          g.share = (float)pt;
+          // NaN sums (no distribution) compare false
+          const double qt = Q ? (g.q.z > 0.0 ? weight(lq, g.q.m, k) / g.q.z : __builtin_nan("")) : 1.0;
+          g.stands = (double)a.accept[row] * qt < pt;
+        }
       }
     }
     __syncthreads();
-    if ((tid & 15) == 0) judged[tid >> 4] = g;
+    if (tid < 256 && (tid & 15) == 0) judged[tid >> 4] = g;
     __syncthreads();
-    const int n = min(16, hi - r0);
-    int i = 0;
-    while (i < n && judged[i].stands) {   // the last row's does not
-      if (c == 0 && tid == 0) {
-        a.out[r0 + i] = judged[i].token;
-        if (a.prob) a.prob[r0 + i] = judged[i].share;
-      }
-      ++i;
+    // the first that does not stand; the sequence's last row does not
+    const int i = __builtin_ctzll(~__ballot(lane < 16 && judged[lane & 15].stands));
+    base = r0;
+    if (i < 16) {
+      stop = r0 + i, end = judged[i];
+    } else if (c == 0 && tid < 16) {
+      a.out[r0 + tid] = judged[tid].token;
+      if (a.prob) a.prob[r0 + tid] = judged[tid].share;
     }
-    if (i < n) stop = r0 + i, end = judged[i];
   }
-  // the new token goes to row `stop`, -1 behind it
-  if (c == 0)
-    for (int r = stop + 1 + tid; r < hi; r += kThreads) {
+  // The other rows' results: drafts that stand, and -1 behind the new token at
+  // row `stop`.  Written late: loads behind a store wait for it, too.
+  auto settle = [&] {
+    if (c > 0) return;
+    if (tid < stop - base) {
+      a.out[base + tid] = judged[tid].token;
+      if (a.prob) a.prob[base + tid] = judged[tid].share;
+    }
+    for (int r = stop + 1 + tid; r < hi; r += THREADS) {
       a.out[r] = -1;
       if (a.prob) a.prob[r] = 0.f;
     }
+  };
   const bool none = !(end.p.z > 0.0);
   if (none || greedy) {
     if (c == 0 && tid == 0) {
@@ -326,135 +348,141 @@ __global__ void __launch_bounds__(kThreads) k_verify_pick(VerifyArgs a) {
       if (a.prob) a.prob[stop] = none ? 0.f : 1.f;
       a.count[seq] = stop - lo + (none ? 0 : 1);
     }
+    settle();
     return;
   }
   const bool fell = stop + 1 < hi;
-  const bool minus = fell && a.q && end.q.z > 0.0;
-  const int less = fell && !a.q && end.token >= 0 && end.token < V ? end.token : -1;
+  const bool minus = Q && fell && end.q.z > 0.0;
+  const int less = !Q && fell && end.token >= 0 && end.token < V ? end.token : -1;
   const void* rp = row_of<F32>(a.p, a.ps, stop);
   const void* rq = minus ? row_of<F32>(a.q, a.qs, stop) : rp;
   const int lead = lead_of<F32>(rp);
+  const double ip = 1.0 / end.p.z, iq = minus ? 1.0 / end.q.z : 0.0;
 
   double w[kVec], pp[kVec];
-  double tr = 0.0, tp = 0.0;
-#pragma unroll 1
-  for (int u = 0; u < U; ++u) {
-    const int i0 = ((c * U + u) * kThreads + tid) * kVec - lead;
-    if (i0 >= V) continue;
+  // weights of this thread's vector of a piece
+  auto weigh = [&](int piece) {
+    const int i0 = (piece * THREADS + tid) * kVec - lead;
     float lp[kVec], lq[kVec];
     load8<F32>(rp, i0, V, lp);
     if (minus) load8<F32>(rq, i0, V, lq);
-    weights8<F32>(lp, lq, end.p, end.q, k, i0, less, minus, w, pp);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) tr += w[j], tp += pp[j];
-  }
+    for (int j = 0; j < kVec; ++j) pp[j] = w[j] = weight(lp[j], end.p.m, k) * ip;
+    if (minus) {
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) tr += shfl_xor(tr, x), tp += shfl_xor(tp, x);
-  if (lane == 0) sr[wave] = tr, sp[wave] = tp;
-  __syncthreads();
-  double* rest = a.rest + (size_t)seq * a.chunks * 2;
-  if (tid == 0) {
-    st_dev64(rest + 2 * c, (sr[0] + sr[1]) + (sr[2] + sr[3]));
-    st_dev64(rest + 2 * c + 1, (sp[0] + sp[1]) + (sp[2] + sp[3]));
+      for (int j = 0; j < kVec; ++j) w[j] = fmax(pp[j] - weight(lq[j], end.q.m, k) * iq, 0.0);
+    } else if (less - i0 >= 0 && less - i0 < kVec) {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) w[j] = i0 + j == less ? 0.0 : w[j];
+    }
+    return i0;
+  };
+  auto sum8 = [&](const double* x) { return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7])); };
+
+  double* rest = a.rest + (size_t)seq * pieces * 2;
+  const int own = Q ? c : (less >= 0 ? (less + lead) / (THREADS * kVec) : -1);
+  double own_sum = 0.0;
+  if (own >= 0) {
+    weigh(own);
+    double tr = sum8(w), tp = Q ? sum8(pp) : 0.0;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) {
+      tr += shfl_xor(tr, x);
+      if (Q) tp += shfl_xor(tp, x);
+    }
+    if (lane == 0) sr[wave] = tr, sp[wave] = tp;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) own_sum += sr[i];
+    if (Q) {
+      if (tid == 0) {
+        st_dev64(rest + 2 * c, own_sum);
+        double p = 0.0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) p += sp[i];
+        st_dev64(rest + 2 * c + 1, p);
+      }
+      const bool last = arrive_last(a.arrived + seq, pieces, &last_flag);
+      settle();
+      if (!last) return;
+    }
   }
-  if (!arrive_last(a.arrived + seq, a.chunks, &last_flag)) return;
 
   // The piece that pick * total falls on, by wave 0: in order, lanes of 64
   // pieces at a time.
   if (wave == 0) {
-    double all = 0.0, allp = 0.0;
-    for (int b = lane; b < a.chunks; b += 64) all += ld_dev64(rest + 2 * b), allp += ld_dev64(rest + 2 * b + 1);
+    const VerifyPart* part = a.part + (size_t)stop * 2 * a.chunks;
+    auto sum_of = [&](int b, bool all_p) {
+      if (b >= pieces) return 0.0;
+      if (Q) return ld_dev64(rest + 2 * b + all_p);
+      // 0 exactly where the largest weight of the piece is, as it comes out below
+      return !all_p && b == own ? own_sum : part[b].z * (weight(part[b].m, end.p.m, k) * ip);
+    };
+    const float r = a.pick[seq];
+    const double mine0 = sum_of(lane, false);
+    double all = mine0;
+    for (int b = lane + 64; b < pieces; b += 64) all += sum_of(b, false);
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) all += shfl_xor(all, x), allp += shfl_xor(allp, x);
-    const int which = all > 0.0 ? 0 : 1;   // nothing left of p - q: p itself
-    const double aim = (double)a.pick[seq] * (which ? allp : all);
+    for (int x = 1; x < 64; x <<= 1) all += shfl_xor(all, x);
+    const bool all_p = !(all > 0.0);   // nothing left of p - q: p itself, whose sum is 1
+    const double aim = (double)r * (all_p ? 1.0 : all);
     double run = 0.0, before = 0.0;
-    int piece = -1, spare = -1;
+    int piece = -1, spare = 0;
     double spare_run = 0.0;
-    for (int b0 = 0; b0 < a.chunks && piece < 0; b0 += 64) {
-      const double mine = b0 + lane < a.chunks ? ld_dev64(rest + 2 * (b0 + lane) + which) : 0.0;
-      double upto = mine;
-#pragma unroll
-      for (int x = 1; x < 64; x <<= 1) {
-        const uint64_t b = __builtin_bit_cast(uint64_t, upto);
-        const uint64_t o = (uint64_t)__shfl_up((uint32_t)(b >> 32), x) << 32 | __shfl_up((uint32_t)b, x);
-        if (lane >= x) upto += __builtin_bit_cast(double, o);
-      }
+    for (int b0 = 0; b0 < pieces && piece < 0; b0 += 64) {
+      const double mine = b0 == 0 && !all_p ? mine0 : sum_of(b0 + lane, all_p), upto = scan64(mine, lane);
       const uint64_t over = __ballot(mine > 0.0 && run + upto > aim), some = __ballot(mine > 0.0);
       const int l = over ? __builtin_ctzll(over) : (some ? 63 - __builtin_clzll(some) : 0);
-      const double excl = upto - mine;
-      const uint64_t eb = __builtin_bit_cast(uint64_t, excl), ub = __builtin_bit_cast(uint64_t, upto);
-      before = run + __builtin_bit_cast(double, (uint64_t)__shfl((uint32_t)(eb >> 32), l) << 32 | __shfl((uint32_t)eb, l));
+      before = run + lane64(upto - mine, l);
       if (over) piece = b0 + l;
       else if (some) spare = b0 + l, spare_run = before;
-      run += __builtin_bit_cast(double, (uint64_t)__shfl((uint32_t)(ub >> 32), 63) << 32 | __shfl((uint32_t)ub, 63));
+      run += lane64(upto, 63);
     }
     if (piece < 0) piece = spare, before = spare_run;   // rounding: the last piece that has any
-    if (lane == 0) found[0] = piece, found[1] = which, left_of[0] = aim - before;
+    if (lane == 0) found[0] = piece, found[1] = all_p, left_of[0] = aim - before;
   }
   __syncthreads();
-  const int piece = found[0], which = found[1];
+  const bool all_p = found[1];
   const double aim = left_of[0];
 
-  // Within it: sums of the vectors, in order.
-  double mine[U], upto[U];
+  // Within it: sums of the vectors, in order.  The first one that passes the
+  // aim, or the last one that has any weight.
+  const int i0 = weigh(found[0]);
+  if (all_p) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int i0 = ((piece * U + u) * kThreads + tid) * kVec - lead;
-    float lp[kVec], lq[kVec];
-    load8<F32>(rp, i0, V, lp);
-    if (minus) load8<F32>(rq, i0, V, lq);
-    weights8<F32>(lp, lq, end.p, end.q, k, i0, less, minus, w, pp);
-    mine[u] = 0.0;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) mine[u] += which ? pp[j] : w[j];
-    upto[u] = mine[u];
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) {
-      const uint64_t b = __builtin_bit_cast(uint64_t, upto[u]);
-      const uint64_t o = (uint64_t)__shfl_up((uint32_t)(b >> 32), x) << 32 | __shfl_up((uint32_t)b, x);
-      if (lane >= x) upto[u] += __builtin_bit_cast(double, o);
-    }
-    if (lane == 63) sr[u * 4 + wave] = upto[u];
+    for (int j = 0; j < kVec; ++j) w[j] = pp[j];
   }
-  if (tid == 0) found[0] = 0x7FFFFFFF, found[1] = -1;
+  const double mine = sum8(w);
+  double upto = scan64(mine, lane);
+  if (lane == 63) sr[wave] = upto;
   __syncthreads();
-  // vectors in order: number (u, tid).  The first one that passes the aim, or
-  // the last one that has any weight.
+  double below = 0.0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    double base = 0.0;
-    for (int i = 0; i < u * 4 + wave; ++i) base += sr[i];
-    upto[u] += base;
-    if (mine[u] > 0.0) {
-      if (upto[u] > aim) atomicMin(&found[0], u * kThreads + tid);
-      atomicMax(&found[1], u * kThreads + tid);
-    }
+  for (int i = 0; i < WAVES - 1; ++i) below += i < wave ? sr[i] : 0.0;
+  upto += below;
+  const uint64_t over = __ballot(mine > 0.0 && upto > aim), some = __ballot(mine > 0.0);
+  if (lane == 0) {
+    first_of[wave] = over ? wave * 64 + __builtin_ctzll(over) : THREADS;
+    last_of[wave] = some ? wave * 64 + 63 - __builtin_clzll(some) : -1;
   }
   __syncthreads();
-  const int hit = found[0] != 0x7FFFFFFF ? found[0] : found[1];
+  int hit = THREADS, last = -1;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (hit != u * kThreads + tid) continue;
-    const int i0 = ((piece * U + u) * kThreads + tid) * kVec - lead;
-    float lp[kVec], lq[kVec];
-    load8<F32>(rp, i0, V, lp);
-    if (minus) load8<F32>(rq, i0, V, lq);
-    weights8<F32>(lp, lq, end.p, end.q, k, i0, less, minus, w, pp);
-    double run = upto[u] - mine[u];
-    int token = -1;
-    double share = 0.0;
-    bool done = false;
+  for (int i = 0; i < WAVES; ++i) hit = min(hit, first_of[i]), last = max(last, last_of[i]);
+  if (hit == THREADS) hit = last;
+  if (!Q) settle();
+  if (tid != hit) return;
+  double run = upto - mine, share = 0.0;
+  int token = -1;
+  bool done = false;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      const double x = which ? pp[j] : w[j];
-      run += x;
-      if (!done && x > 0.0) token = i0 + j, share = pp[j], done = run > aim;
-    }
-    a.out[stop] = token;
-    if (a.prob) a.prob[stop] = (float)share;
-    a.count[seq] = stop - lo + 1;
+  for (int j = 0; j < kVec; ++j) {
+    run += w[j];
+    if (!done && w[j] > 0.0) token = i0 + j, share = pp[j], done = run > aim;
   }
+  a.out[stop] = token;
+  if (a.prob) a.prob[stop] = (float)share;
+  a.count[seq] = stop - lo + 1;
 }
 
 }  // namespace
@@ -462,11 +490,14 @@ __global__ void __launch_bounds__(kThreads) k_verify_pick(VerifyArgs a) {
 int launch_verify(const VerifyArgs& a) {
   hipStream_t st = reinterpret_cast<hipStream_t>(a.stream);
   const unsigned rows = (unsigned)a.n * (a.q ? 2u : 1u);
-  const dim3 g1(rows * (unsigned)a.chunks), g2((unsigned)a.seqs * (unsigned)a.chunks), b(kThreads);
-#define DC_VERIFY(F32_, U_)                                                            \
-  do {                                                                                 \
-    if (a.n > 0) hipLaunchKernelGGL((k_verify_stats<F32_, U_>), g1, b, 0, st, a);      \
-    hipLaunchKernelGGL((k_verify_pick<F32_, U_>), g2, b, 0, st, a);                    \
+  const dim3 g1(rows * (unsigned)a.chunks);
+#define DC_VERIFY(F32_, U_)                                                                                          \
+  do {                                                                                                               \
+    if (a.n > 0) hipLaunchKernelGGL((k_verify_stats<F32_, U_>), g1, dim3(kThreads), 0, st, a);                       \
+    if (a.q)                                                                                                         \
+      hipLaunchKernelGGL((k_verify_pick<F32_, true, pick_threads(U_)>), dim3((unsigned)a.seqs * a.pieces), dim3(pick_threads(U_)), 0, st, a); \
+    else                                                                                                             \
+      hipLaunchKernelGGL((k_verify_pick<F32_, false, U_ * kThreads>), dim3(a.seqs), dim3(U_ * kThreads), 0, st, a);   \
   } while (0)
   if (a.f32) {
     if (a.vecs == 4) DC_VERIFY(true, 4); else DC_VERIFY(true, 1);

@@ -20,8 +20,9 @@ VerifyPlan verify_plan(int32_t vocab, int32_t N, int32_t seqs) {
   auto chunks = [&](int32_t per) { return (vecs + kVerifyThreads * per - 1) / (kVerifyThreads * per); };
   p.vecs = chunks(4) * N >= 512 ? 4 : 1;
   p.chunks = (int32_t)chunks(p.vecs);
+  p.pieces = (int32_t)chunks(pick_threads(p.vecs) / kVerifyThreads);
   p.rest_off = round_up(sizeof(VerifyPart) * 2 * (size_t)N * p.chunks, kAlign);
-  p.arrived_off = p.rest_off + round_up(2 * sizeof(double) * (size_t)seqs * p.chunks, kAlign);
+  p.arrived_off = p.rest_off + round_up(2 * sizeof(double) * (size_t)seqs * p.pieces, kAlign);
   p.ws = p.arrived_off + round_up(4 * (size_t)seqs, kAlign);
   return p;
 }
@@ -159,6 +160,7 @@ dc_status dc_verify_drafts(const dc_verify_batch* b, int32_t dtype, int32_t voca
   a.count = count;
   a.prob = prob;
   a.part = reinterpret_cast<VerifyPart*>(base);
+  a.pieces = plan.pieces;
   a.rest = reinterpret_cast<double*>(base + plan.rest_off);
   a.arrived = reinterpret_cast<uint32_t*>(base + plan.arrived_off);
   a.vocab = vocab;

@@ -19,6 +19,7 @@ struct alignas(16) VerifyPart {
 
 constexpr int kVerifyVec = 8;       // logits of a vector
 constexpr int kVerifyThreads = 256;
+constexpr int pick_threads(int vecs) { return vecs == 4 ? 2 * kVerifyThreads : kVerifyThreads; }
 
 struct VerifyArgs {
   const void *p, *q;                // target, draft (null: none)
@@ -28,13 +29,13 @@ struct VerifyArgs {
   int32_t *out, *count;
   float* prob;
   VerifyPart* part;                 // [N][2][chunks]
-  double* rest;                     // [seqs][chunks][2]: sums of max(p - q, 0) and of p
+  double* rest;                     // [seqs][pieces][2]: sums of max(p - q, 0) and of p
   uint32_t* arrived;                // [seqs]
-  int32_t vocab, n, seqs, chunks, vecs, f32;   // vecs: vectors of a thread in a chunk
+  int32_t vocab, n, seqs, chunks, vecs, pieces, f32;   // vecs: vectors of a thread in a chunk; pieces: of one vector of pick_threads
   void* stream;
 };
 struct VerifyPlan {
-  int32_t vecs, chunks;
+  int32_t vecs, chunks, pieces;
   size_t rest_off, arrived_off, ws;
 };
 VerifyPlan verify_plan(int32_t vocab, int32_t N, int32_t seqs);
