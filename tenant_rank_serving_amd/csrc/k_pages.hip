@@ -55,9 +55,17 @@ __device__ __forceinline__ int upto_lane(int v) {
 // need is known, and the free pages, in the order of their numbers, are dealt
 // to the sequences, in theirs: the k-th one to the sequence among whose running
 // needs k falls.
+//
+// Bound by latency: lengths, entries, counts and free pages are read one after
+// the other, about a microsecond each.  48 of 64 sequences giving back 5000 pages
+// (whose counts one CU's path to the L2 takes one by one) 12 us, growing by 255
+// pages out of 6100 9 us.
 __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const int32_t* new_len, int32_t* copies) {
-  // per sequence: pages needed up to and with it, and whether the first of its own is for an exchange
+  // per sequence: pages needed up to and with it, and whether the first of its own is for an exchange;
+  // its old length
   __shared__ uint32_t upto[DC_KV_MAX_SEQS];
+  __shared__ int32_t old_of[DC_KV_MAX_SEQS];
+  __shared__ int32_t given[kResizeThreads];   // what the first sequences get for their shared pages
   __shared__ int box[kWaves];
   __shared__ uint32_t status;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -66,22 +74,73 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   if (tid == 0) status = 0;
   __syncthreads();
 
-  for (int b = wave; b < t.seqs; b += kWaves) {
-    const int old = t.kv_len[b], want = new_len[b];
-    if (old < 0 || old > most || want < 0 || want > most) {
-      if (lane == 0) atomicOr(&status, (uint32_t)DC_KV_BAD);
-      continue;
+  // the first kResizeThreads sequences' lengths and shared pages, for later
+  int old0 = 0, want0 = 0;
+  int32_t shared0 = -1;
+  if (tid < t.seqs) {
+    old0 = t.kv_len[tid], want0 = new_len[tid];
+    if (old0 >= 0 && old0 < want0 && want0 <= most && (old0 & (t.page - 1))) shared0 = t.pages[(int64_t)tid * t.width + (old0 >> shift)];
+  }
+  // 64 sequences of a wave at a time, a length in each lane; then those that give
+  // pages back, 256 entries of one at a time, with the next ones' on their way
+  for (int s0 = wave; s0 < t.seqs; s0 += 64 * kWaves) {
+    const int b = s0 + lane * kWaves;
+    int from = 0, to = 0;
+    if (b < t.seqs) {
+      const int old = t.kv_len[b], want = new_len[b];
+      if (old < 0 || old > most || want < 0 || want > most) atomicOr(&status, (uint32_t)DC_KV_BAD);
+      else from = pages_of(want), to = pages_of(old);
     }
-    int32_t* row = t.pages + (int64_t)b * t.width;
-    for (int i = pages_of(want) + lane; i < pages_of(old); i += 64) {
-      const int32_t p = row[i];
-      if (p >= 0 && p < t.num_pages) add_agent(t.refs + p, -1);
-      else atomicOr(&status, (uint32_t)DC_KV_BAD);
-      row[i] = -1;
+    uint64_t todo = __ballot(from < to);
+    if (!todo) continue;
+    int l = __builtin_ctzll(todo), at = __builtin_amdgcn_readlane(from, l), end = __builtin_amdgcn_readlane(to, l);
+    int32_t e[4], after[4];
+    auto load = [&](int32_t* x) {
+      const int32_t* row = t.pages + (int64_t)(s0 + l * kWaves) * t.width;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = at + 64 * j + lane < end ? row[at + 64 * j + lane] : 0;
+    };
+    load(e);
+    for (;;) {
+      const int l_ = l, at_ = at, end_ = end;
+      at += 256;
+      if (at >= end) {
+        todo &= todo - 1;
+        if (todo) l = __builtin_ctzll(todo), at = __builtin_amdgcn_readlane(from, l), end = __builtin_amdgcn_readlane(to, l);
+      }
+      if (todo) load(after);
+      int32_t* row = t.pages + (int64_t)(s0 + l_ * kWaves) * t.width;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = at_ + 64 * j + lane;
+        if (i >= end_) continue;
+        if (e[j] >= 0 && e[j] < t.num_pages) add_agent(t.refs + e[j], -1);
+        else atomicOr(&status, (uint32_t)DC_KV_BAD);
+        row[i] = -1;
+      }
+      if (!todo) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = after[j];
     }
   }
   __builtin_amdgcn_s_waitcnt(0);   // the counts have fallen
   __syncthreads();
+
+  // the free pages: 4 a thread, the next ones on their way while these are dealt
+  const int vecs = (t.num_pages + 3) / 4;
+  auto load = [&](int v) {
+    int4 r = int4{1, 1, 1, 1};
+    if (4 * v + 3 < t.num_pages) r = reinterpret_cast<const int4*>(t.refs)[v];
+    else if (v < vecs) {
+      r.x = t.refs[4 * v];
+      if (4 * v + 1 < t.num_pages) r.y = t.refs[4 * v + 1];
+      if (4 * v + 2 < t.num_pages) r.z = t.refs[4 * v + 2];
+    }
+    return r;
+  };
+  // (the counts that fell are in the L2; nothing of them is in this CU's L1 yet)
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  int4 now = load(tid), next = load(kResizeThreads + tid);
 
   int total = 0;
   for (int b0 = 0; b0 < t.seqs; b0 += kResizeThreads) {
@@ -89,11 +148,12 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
     int need = 0;
     bool swap = false;
     if (b < t.seqs) {
-      const int old = t.kv_len[b], want = new_len[b];
+      const int old = b0 ? t.kv_len[b] : old0, want = b0 ? new_len[b] : want0;
+      old_of[b] = old;
       if (old >= 0 && old <= most && want > old && want <= most) {
         need = pages_of(want) - pages_of(old);
         if (old & (t.page - 1)) {
-          const int32_t p = t.pages[(int64_t)b * t.width + (old >> shift)];
+          const int32_t p = b0 ? t.pages[(int64_t)b * t.width + (old >> shift)] : shared0;
           if (p >= 0 && p < t.num_pages) swap = ld_agent(t.refs + p) > 1;
           else atomicOr(&status, (uint32_t)DC_KV_BAD);
           need += swap;
@@ -109,22 +169,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   }
   __syncthreads();
 
-  // the free pages: 4 a thread, the next ones on their way while these are dealt
   int dealt = 0;
-  const int vecs = (t.num_pages + 3) / 4;
-  auto load = [&](int v) {
-    int4 r = int4{1, 1, 1, 1};
-    if (4 * v + 3 < t.num_pages) r = reinterpret_cast<const int4*>(t.refs)[v];
-    else if (v < vecs) {
-      r.x = t.refs[4 * v];
-      if (4 * v + 1 < t.num_pages) r.y = t.refs[4 * v + 1];
-      if (4 * v + 2 < t.num_pages) r.z = t.refs[4 * v + 2];
-    }
-    return r;
-  };
-  // (the counts that fell are in the L2; nothing of them is in this CU's L1 yet)
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  int4 now = load(tid), next = load(kResizeThreads + tid);
   for (int v0 = 0; v0 < vecs && dealt < total; v0 += kResizeThreads) {
     const int4 later = load(v0 + 2 * kResizeThreads + tid);
     const int r[4] = {now.x, now.y, now.z, now.w};
@@ -146,12 +191,16 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
         }
         const int slot = k - (lo ? (int)(upto[lo - 1] >> 1) : 0);
         const bool swap = upto[lo] & 1;
-        const int old = t.kv_len[lo];
+        const int old = old_of[lo];
         int32_t* row = t.pages + (int64_t)lo * t.width;
         if (swap && slot == 0) {
-          copies[2 * lo] = row[old >> shift];
-          copies[2 * lo + 1] = p;
-          row[old >> shift] = p;
+          if (lo < kResizeThreads) {
+            given[lo] = p;
+          } else {
+            copies[2 * lo] = row[old >> shift];
+            copies[2 * lo + 1] = p;
+            row[old >> shift] = p;
+          }
         } else {
           row[pages_of(old) + slot - swap] = p;
         }
@@ -169,7 +218,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   for (int b0 = 0; b0 < t.seqs; b0 += kResizeThreads) {
     const int b = b0 + tid;
     if (b >= t.seqs) continue;
-    const int old = t.kv_len[b], want = new_len[b];
+    const int old = old_of[b], want = b0 ? new_len[b] : want0;
     if (old < 0 || old > most || want < 0 || want > most) continue;
     const int end = (int)(upto[b] >> 1), first = b ? (int)(upto[b - 1] >> 1) : 0;
     const bool swap = upto[b] & 1;
@@ -179,9 +228,13 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
       for (int k = first; k < have; ++k) {
         const int slot = k - first;
         if (swap && slot == 0) {
-          t.refs[copies[2 * b + 1]] = 0;
-          row[old >> shift] = copies[2 * b];
-          copies[2 * b] = copies[2 * b + 1] = -1;
+          if (b0 == 0) {
+            t.refs[given[tid]] = 0;
+          } else {
+            t.refs[copies[2 * b + 1]] = 0;
+            row[old >> shift] = copies[2 * b];
+            copies[2 * b] = copies[2 * b + 1] = -1;
+          }
         } else {
           int32_t* e = row + pages_of(old) + slot - swap;
           t.refs[*e] = 0;
@@ -190,7 +243,14 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
       }
       continue;
     }
-    if (swap) add_agent(t.refs + copies[2 * b], -1);
+    if (swap) {
+      if (b0 == 0) {
+        copies[2 * b] = shared0;
+        copies[2 * b + 1] = given[tid];
+        t.pages[(int64_t)b * t.width + (old >> shift)] = given[tid];
+      }
+      add_agent(t.refs + (b0 ? copies[2 * b] : shared0), -1);
+    }
     t.kv_len[b] = want;
   }
   __syncthreads();
