@@ -884,10 +884,12 @@ dc_status dc_kv_resize(const dc_kv_table* t, const int32_t* new_len, int32_t* co
 /*
  * dc_kv_fork -- row dst[i] becomes a branch of row src[i]: the same pages
  * (refs + 1 each) and length, nothing copied (dc_kv_resize exchanges the last
- * page when one of them grows).  dst[i] has to be empty (kv_len 0, else
- * DC_KV_BAD and left out); a row may be src any number of times, dst once, and
- * not both.
- *   src, dst  device int32 [n]
+ * page when one of them grows).  dst[i] has to be empty.  A row may be src any
+ * number of times, dst once, and not both.  What breaks this is left out, with
+ * DC_KV_BAD: a dst whose length is not 0, one that stands in front of it in the
+ * list too, and a src that is dst anywhere.
+ *   src, dst  device int32 [n], n <= DC_KV_MAX_SEQS (else DC_ERR_UNSUPPORTED)
+ * Errors otherwise as for dc_kv_resize.
  */
 dc_status dc_kv_fork(const dc_kv_table* t, const int32_t* src, const int32_t* dst, int32_t n, uint32_t* status,
                      void* stream);

@@ -137,9 +137,9 @@ class Tables:
         return copies
 
     def fork(self, src, dst):
-        for s, d in zip(src, dst):
+        for i, (s, d) in enumerate(zip(src, dst)):
             n = len(self.pages)
-            if not (0 <= s < n and 0 <= d < n and s != d and self.kv_len[d] == 0
+            if s in dst or d in dst[:i] or not (0 <= s < n and 0 <= d < n and s != d and self.kv_len[d] == 0
                     and 0 <= self.kv_len[s] <= len(self.pages[0]) * self.page):
                 self.bad = True
                 continue

@@ -257,16 +257,22 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   if (tid == 0 && status) atomicOr(t.status, status);
 }
 
-// Block: one branch.
-__global__ void __launch_bounds__(256) k_fork(TableArgs t, const int32_t* src, const int32_t* dst) {
+// Block: one branch.  Every block looks through all of dst for rows that the call
+// writes twice, or reads and writes.
+__global__ void __launch_bounds__(256) k_fork(TableArgs t, const int32_t* src, const int32_t* dst, int count) {
   const int s = src[blockIdx.x], d = dst[blockIdx.x], tid = threadIdx.x;
+  bool meets = false;
+  for (int j = tid; j < count; j += 256) {
+    const int other = dst[j];
+    meets |= other == s || (other == d && j < (int)blockIdx.x);
+  }
   bool ok = s >= 0 && s < t.seqs && d >= 0 && d < t.seqs && s != d;
   int n = 0;
   if (ok) {
     n = t.kv_len[s];
     ok = n >= 0 && n <= t.width * t.page && t.kv_len[d] == 0;
   }
-  __syncthreads();   // everyone has read the lengths
+  ok = !__syncthreads_or(meets) && ok;   // (everyone has read the lengths)
   if (!ok) {
     if (tid == 0) atomicOr(t.status, (uint32_t)DC_KV_BAD);
     return;
@@ -421,7 +427,7 @@ int launch_resize(const TableArgs& t, const int32_t* new_len, int32_t* copies) {
 }
 
 int launch_fork(const TableArgs& t, const int32_t* src, const int32_t* dst, int32_t n) {
-  hipLaunchKernelGGL(k_fork, dim3((unsigned)n), dim3(256), 0, reinterpret_cast<hipStream_t>(t.stream), t, src, dst);
+  hipLaunchKernelGGL(k_fork, dim3((unsigned)n), dim3(256), 0, reinterpret_cast<hipStream_t>(t.stream), t, src, dst, n);
   return (int)hipGetLastError();
 }
 

@@ -194,7 +194,7 @@ dc_status dc_kv_fork(const dc_kv_table* t, const int32_t* src, const int32_t* ds
   const dc_status st = check_table(t, status, stream, &a);
   if (st != DC_OK) return st;
   if (n < 0) return DC_ERR_INVALID_ARG;
-  if (n > kMostBlocks) return DC_ERR_UNSUPPORTED;
+  if (n > DC_KV_MAX_SEQS) return DC_ERR_UNSUPPORTED;   // (every block looks through dst)
   if (n == 0) return DC_OK;
   if (!src || !dst) return DC_ERR_INVALID_ARG;
   if (!aligned(src, 4) || !aligned(dst, 4)) return DC_ERR_ALIGN;

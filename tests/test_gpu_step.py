@@ -373,6 +373,21 @@ def test_tables_numbers_out_of_range():
     assert t.status.item() == trs.DC_KV_BAD
 
 
+@pytest.mark.parametrize("n", [6, 400])
+def test_fork_same_row_twice(n):
+    """A row that is dst twice takes the first branch alone, a row that is both src and dst none."""
+    note("tables, rows named twice", n)
+    rng = np.random.default_rng(n)
+    t = start_table(rng, n + 4, 3, 16, 16, 2)
+    t.resize(np.array([40, 20, 0, 0] + [0] * n))
+    src = np.concatenate([[0, 1, 2, 0, 1, 3], rng.integers(0, 6, n - 6)])
+    dst = np.concatenate([[2, 2, 5, 4, 5, 3], rng.integers(4, n + 4, n - 6)])
+    t.fork(src, dst)
+    assert t.status.item() == trs.DC_KV_BAD and t.lens[:6].tolist() == [40, 20, 40, 0, 40, 0]
+    t.resize(np.zeros(n + 4, np.int32))
+    assert (t.refs.cpu().numpy() > 0).sum() == 2
+
+
 def test_tables_captured():
     """A captured fork and resize follow the lengths that changed; new_len may be kv_len itself."""
     t = torch()

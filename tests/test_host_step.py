@@ -117,6 +117,7 @@ def test_resize_refusals(L, kw, want):
     (dict(n=1, src=0x4001), E.DC_ERR_ALIGN), (dict(n=1, dst=0x5002), E.DC_ERR_ALIGN), (dict(n=1 << 24), E.DC_ERR_UNSUPPORTED),
     (dict(n=1, src=0x2000), E.DC_ERR_INVALID_ARG), (dict(n=4, dst=0x3000 - 8), E.DC_ERR_INVALID_ARG),
     (dict(n=1, status=0x4000), E.DC_ERR_INVALID_ARG),
+    (dict(n=16385), E.DC_ERR_UNSUPPORTED),
 ])
 def test_fork_refusals(L, kw, want):
     assert fork(L, **kw) == want
