@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   if (tid == 0 && status) atomicOr(t.status, status);
 }
 
-// Block: one branch.  Every block looks through all of dst for rows that the call
+// Block: one branch.  Bound by latency, 4 us.  Every block looks through all of dst for rows that the call
 // writes twice, or reads and writes.
 __global__ void __launch_bounds__(256) k_fork(TableArgs t, const int32_t* src, const int32_t* dst, int count) {
   const int s = src[blockIdx.x], d = dst[blockIdx.x], tid = threadIdx.x;
@@ -308,7 +308,11 @@ __device__ __forceinline__ int64_t piece_at(const LayerArgs& a, int u) {
   return h * a.head_stride + s * a.slot_stride + 16 * c;
 }
 
-// Block: 16 KiB of a page of one layer's keys or values.
+// Block: 16 KiB of a page of one layer's keys or values, 4 pieces a thread on their
+// way at once.  Bound by HBM: 96 pages of 64 tokens of 32 layers x 8 heads (e4m3,
+// 0.4 GB moved twice) 159 us, 5.1 TB/s, the rate of a large copy; 4 pages of 32 x 32
+// heads of 128 bf16 numbers 15 us of which 13 are its bytes.  Addressing a page
+// without gaps as one piece saves the division and the shifts (23 -> 15 us there).
 template <bool Whole>
 __global__ void __launch_bounds__(256) k_copy(LayerArgs a, const int32_t* copies) {
   const int64_t from = copies[2 * blockIdx.x], to = copies[2 * blockIdx.x + 1];
@@ -340,7 +344,9 @@ __device__ __forceinline__ int64_t token_at(const LayerArgs& a, const int32_t* t
 }
 
 // Block: 64 kept tokens of 64 >> a.pieces heads of one layer's keys or values, 16
-// pieces of 16 bytes a thread.  To other pages the blocks are independent.  In
+// pieces of 16 bytes a thread.  Bound by HBM: 500 of 1000 tokens of 32 layers x 8
+// heads 30 us (25 at a large copy's rate), 8 chats of 4000 395 us (373); with 4
+// pieces a thread and a look-up for each 60 and 594.  To other pages the blocks are independent.  In
 // place one block moves a sequence's tokens, a tile after the other: sources
 // ascend and lie at or behind their places, so a tile's places hold nothing that
 // is still to be read once the tile itself has been.  The next tile's places are
