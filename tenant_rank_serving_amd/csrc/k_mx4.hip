@@ -238,15 +238,16 @@ int launch_mx4(const Mx4Args& a) {
 //   4096 x 4096: 32 tokens 16x32 3.4, 32x32 3.7; 64 tokens 16x32 4.3, 32x32 3.9;
 //   128 tokens 32x64 5.1, 32x32 5.3, 64x64 6.3; 256 tokens 64x64 6.6, 32x64 7.1;
 //   512 tokens 64x64 9.0, 64x128 9.0, 128x128 11.7; 1024 tokens 64x128 12.8,
-//   128x128 12.5; 4096 tokens 128x128 33.7, 256x256 34.5, 64x128 40.2
-//   4096 x 11008: 128 tokens 32x64 9.1, 64x64 11.4; 8192 tokens 128x128 150.8,
-//   256x256 138.6; 11008 x 4096: 64 tokens 64x64 6.5, 32x64 7.5; 8192 tokens
-//   128x128 163.9, 256x256 170.6; 32000 x 4096, 8192 tokens 480.8 and 427.9
+//   128x128 12.5; 4096 x 11008: 128 tokens 32x64 9.1, 64x64 11.4; 11008 x 4096: 64
+//   tokens 64x64 6.5, 32x64 7.5 (codes drawn evenly); with normal numbers, 128x128
+//   and 256x256: 4096 x 4096 2048 tokens 21.6 and 30.5, 4096 42.3 and 40.2, 8192
+//   84.9 and 78.7; 11008 x 4096 2048 tokens 57 and 62, 4096 118 and 108, 8192 219
+//   and 212; 32000 x 4096, 8192 tokens 588 and 516
 int launch_mx4q(const Mx4Args& a) {
   constexpr struct {
     int rows, toks, first, end, step;
   } kTiles[] = {{16, 16, 2200, 0, 32}, {16, 32, 2300, 0, 35},    {32, 32, 2100, 0, 48},      {32, 64, 2600, 0, 70},
-                {64, 64, 3200, 0, 92}, {64, 128, 3400, 0, 148}, {128, 128, 2000, 1600, 200}, {256, 256, 2000, 5000, 770}};
+                {64, 64, 3200, 0, 92}, {64, 128, 3400, 0, 148}, {128, 128, 2000, 1600, 200}, {256, 256, 2000, 5000, 730}};
   int best = 0;
   int64_t least = INT64_MAX;
   for (int c = 0; c < 8; ++c) {

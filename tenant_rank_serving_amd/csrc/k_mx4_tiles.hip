@@ -14,14 +14,19 @@
 // in LDS such that they lie in different banks.
 //
 // Blocks stay for several tiles and load the next one's first steps under the last
-// one's products.  Measured, 16384 tokens x 11008 x 4096 (1.48 TFLOP): 384 us with a
-// model's numbers, 3.8 PFLOP/s, and 331 with codes drawn evenly; blocks of one tile
-// 369 there, without writing results 297, without loads 307, without reading LDS
-// 319, products alone 221 (245 with a model's numbers: the clock falls under them).
-// Bound by these taking turns: two waves a SIMD, which meet at a barrier every step.
-// Results go out as 64 bytes a token, past the caches: 16-byte pieces cost 10 %
-// more, cached stores 7 %.  Not faster: wave tiles of 128 x 128 (the compiler moves
-// their sums about).
+// one's products.  The largest tile has two waves a SIMD, which take turns: while
+// one multiplies, the other reads the operands of its next step and sends for
+// tiles.  (All waves reading, then all multiplying: 398 us where this takes 360,
+// 32000 x 4096 with 8192 tokens 548 and 516; and operands of two steps in registers
+// at once, 7 more than there are.)
+//
+// Measured, 16384 tokens x 11008 x 4096 (1.48 TFLOP), normal numbers: 355 to 375 us,
+// 4.0 PFLOP/s.  Bound by the power that the card may take: without writing results
+// 315, without loads 327, with operands that stay 290, products alone 214, at 1.6
+// GHz.  Not faster: results written over the next tile's steps instead of at once
+// (361), products of 32 x 32 x 64 (365), wave tiles of 128 x 128 (the compiler moves
+// their sums about).  Results go out as 64 bytes a token, past the caches: 16-byte
+// pieces cost 10 % more, 32-byte pieces 70 %, cached stores 3 %.
 #include <hip/hip_runtime.h>
 
 #include "step.h"
@@ -51,8 +56,8 @@ struct TilesLds {
   alignas(256) uint8_t bs[TB * kBs];
 };
 
-// wait_barrier, or as many loads as there are where `fresh`.  (The branch is hidden
-// from the compiler, which makes copies of the steps for either side.)
+// wait_barrier, or M more or as many loads as there are where `fresh`.  (The branch
+// is hidden from the compiler, which makes copies of the steps for either side.)
 template <int N>
 __device__ __forceinline__ void wait_barrier_unless(int fresh) {
   asm volatile(
@@ -60,6 +65,16 @@ __device__ __forceinline__ void wait_barrier_unless(int fresh) {
       "n"(N)
       : "memory", "scc");
 }
+
+template <int N, int M>
+__device__ __forceinline__ void wait_barrier_more(int fresh) {
+  asm volatile(
+      "s_waitcnt vmcnt(%2)\n\ts_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lmore%=\n\ts_waitcnt vmcnt(%1)\n.Lmore%=:\n\ts_waitcnt "
+      "lgkmcnt(0)\n\ts_barrier" ::"s"(__builtin_amdgcn_readfirstlane(fresh)),
+      "n"(N), "n"(N + M)
+      : "memory", "scc");
+}
+__device__ __forceinline__ void only_barrier() { asm volatile("s_barrier" ::: "memory"); }
 
 template <int MA, int NB>
 struct Operands {
@@ -92,6 +107,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WAVES) k_mx4_tiles(Mx4Args g, in
   static_assert(LA * WN == MA && LB * WM == NB, "every wave loads as many tiles");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
+  constexpr bool TURNS = WM * WN == 8;   // waves w and w + 4 share a SIMD and take turns
   const int gc = g.in / 128, hc = (gc + 3) / 4, rts = g.out / 16, tts = (g.T + 15) / 16;
   // The 8 XCDs take consecutive blocks in turn; each gets a stretch of the tiles
   // in an order where blocks that run together share rows and tokens: bands of
@@ -167,19 +183,23 @@ __global__ void __launch_bounds__(64 * WM * WN, WAVES) k_mx4_tiles(Mx4Args g, in
   if (j >= until) return;
   place(j, &m, &n);
   Src now = sources(m, n);
-  Operands<MA, NB> o[2];
+  Operands<MA, NB> o[TURNS ? 1 : 2];
   auto begin = [&] {
     load_scales(now, 0);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) load(now, min(s, gc - 1), s);
+    for (int s = 0; s < (TURNS ? NS - 1 : NS); ++s) load(now, min(s, gc - 1), s);
     wait_barrier<0>();
-    fetch(o[0], 0);
-    fetch_scales(sa, sb);
+    if constexpr (!TURNS) {
+      fetch(o[0], 0);
+      fetch_scales(sa, sb);
+    }
   };
   begin();
+  // from here on the second four are a barrier behind
+  if (TURNS && wave >= 4) only_barrier();
   const bool whole = gc % 4 == 0;   // else a tile's last steps send for nothing, and the next tile begins anew
 
-  constexpr int L = LA + LB;
+  constexpr int L = LA + LB, STORES = MA / 2 * NB;
   // Step J of four (which scale byte, which operands and place in LDS), k + J of
   // the tile; it sends for the step 4 later, of the next tile at the end.  What
   // may be on its way as a step begins: the tiles sent for since those of the
@@ -198,6 +218,34 @@ __global__ void __launch_bounds__(64 * WM * WN, WAVES) k_mx4_tiles(Mx4Args g, in
         acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(piece(o[J & 1].a[a]), piece(o[J & 1].b[b]), acc[a][b], \
                                                                     kFp4, kFp4, J, sa[a], J, sb[b]);                        \
   }
+  // The same in turns, in two halves with a barrier behind each: reading, and
+  // sending for the tile 3 steps later (the place of the step before, which the
+  // other four have read by then), then multiplying.  The next step's tile has to
+  // be here at the first barrier, and the scales, sent for in step 1, at step 3's.
+  // In a tile's first two steps the tiles have to be that were sent for before the
+  // last one's results: STORES more may be on their way.  (As many stores as that
+  // there are, or none older than those loads: below.)
+#define DC_TURN(J)                                                                                                          \
+  {                                                                                                                         \
+    fetch(o[0], J);                                                                                                         \
+    if (J == 0) fetch_scales(sa, sb);                                                                                       \
+    if (J == 1) load_scales(src, min(ahead >> 2, hc - 1));                                                                  \
+    load(src, min(ahead + J - 1, gc - 1), (J + NS - 1) % NS);                                                               \
+    __builtin_amdgcn_sched_barrier(0);                                                                                      \
+    if (J < 2) wait_barrier_more<J == 0 ? 2 * L : 3 * L, STORES>(fresh);                                                    \
+    else wait_barrier<J == 2 ? 3 * L : 2 * L>();                                                                            \
+    __builtin_amdgcn_sched_barrier(0);                                                                                      \
+    arrived(o[0]);                                                                                                          \
+    __builtin_amdgcn_s_setprio(1);                                                                                          \
+    _Pragma("unroll") for (int b = 0; b < NB; ++b)                                                                          \
+      _Pragma("unroll") for (int a = 0; a < MA; ++a)                                                                        \
+        acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(piece(o[0].a[a]), piece(o[0].b[b]), acc[a][b],         \
+                                                                    kFp4, kFp4, J, sa[a], J, sb[b]);                        \
+    __builtin_amdgcn_s_setprio(0);                                                                                          \
+    __builtin_amdgcn_sched_barrier(0);                                                                                      \
+    only_barrier();                                                                                                         \
+    __builtin_amdgcn_sched_barrier(0);                                                                                      \
+  }
   for (;;) {
     int nm = m, nn = n;
     const bool more = j + stride < until;
@@ -213,6 +261,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WAVES) k_mx4_tiles(Mx4Args g, in
 #pragma clang loop unroll(disable)
     for (; k + 4 <= gc; k += 4) {   // no branch among the products: the sums stay where they are
       int ahead = k + 4;            // what is sent for
+      if constexpr (TURNS) DC_TURN(0)   // (the last of this tile)
       uint32_t over = whole && ahead >= gc ? ~0u : 0u;
       over = __builtin_amdgcn_readfirstlane(over);   // (no copy of the steps for this either)
       ahead &= ~over;
@@ -220,25 +269,41 @@ __global__ void __launch_bounds__(64 * WM * WN, WAVES) k_mx4_tiles(Mx4Args g, in
       for (int i = 0; i < LA; ++i) src.a[i] += (now.a[i] - src.a[i]) & over, src.as[i] += (now.as[i] - src.as[i]) & over;
 #pragma unroll
       for (int i = 0; i < LB; ++i) src.b[i] += (now.b[i] - src.b[i]) & over, src.bs[i] += (now.bs[i] - src.bs[i]) & over;
-      DC_STEP(0)
-      DC_STEP(1)
-      DC_STEP(2)
-      DC_STEP(3)
-      fresh = 0;
-      fetch_scales(sa, sb);   // of the next four steps: here since step 3's barrier
+      if constexpr (TURNS) {
+        DC_TURN(1)
+        DC_TURN(2)
+        DC_TURN(3)
+        fresh = 0;
+      } else {
+        DC_STEP(0)
+        DC_STEP(1)
+        DC_STEP(2)
+        DC_STEP(3)
+        fresh = 0;
+        fetch_scales(sa, sb);   // of the next four steps: here since step 3's barrier
+      }
     }
     if (k < gc) {
       const int ahead = k + 4;
-      DC_STEP(0)
-      if (k + 1 < gc) {
-        DC_STEP(1)
-        if (k + 2 < gc) DC_STEP(2)
+      if constexpr (TURNS) {
+        DC_TURN(0)
+        if (k + 1 < gc) {
+          DC_TURN(1)
+          if (k + 2 < gc) DC_TURN(2)
+        }
+      } else {
+        DC_STEP(0)
+        if (k + 1 < gc) {
+          DC_STEP(1)
+          if (k + 2 < gc) DC_STEP(2)
+        }
       }
     }
-    // the next tile's first tiles are here before the results leave: loads and
-    // stores are counted together
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // Loads and stores are counted together: the next tile's first tiles are here
+    // before the results leave, unless (in turns) all STORES of them will and more
+    // tiles follow.
     const int r0 = m * TA * 16 + wm * MA * 16;
+    if (!TURNS || !whole || !more || r0 >= g.out || (n * TB + (wn + 1) * NB - 1) * 16 >= g.T) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if (r0 < g.out) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -258,10 +323,17 @@ __global__ void __launch_bounds__(64 * WM * WN, WAVES) k_mx4_tiles(Mx4Args g, in
     j += stride;
     m = nm, n = nn;
     if (!whole) {
-      wait_barrier<0>();   // everyone has left the last tile's operands
-      begin();
+      if constexpr (TURNS) {
+        begin();          // everyone has read the last tile's operands: the other four before this half
+        only_barrier();   // and their loads are here
+      } else {
+        wait_barrier<0>();   // everyone has left the last tile's operands
+        begin();
+      }
     }
   }
+  if (TURNS && wave < 4) only_barrier();
+#undef DC_TURN
 #undef DC_STEP
 }
 

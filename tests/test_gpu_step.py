@@ -726,6 +726,12 @@ def test_apply_mx4q_tiles(t_, out, inn):
     assert t.equal(y[:t_], first[:t_])
 
 
+# The largest tile: two or three for a block, columns of whole groups of 512 and of 1, 2 and 3 more.
+@pytest.mark.parametrize("t_,out,inn", [(5300, 5888, 1408), (4500, 10496, 1280), (5800, 7936, 1536), (6300, 6912, 1664), (4600, 6272, 2048)])
+def test_apply_mx4q_largest_tiles(t_, out, inn):
+    test_apply_mx4q_tiles(t_, out, inn)
+
+
 @pytest.mark.parametrize("t_", [1, 20, 70, 300])
 def test_mx4_values_that_are_not_finite(t_):
     """A NaN block reaches its row, an x that is not finite its token; neither reaches further."""
