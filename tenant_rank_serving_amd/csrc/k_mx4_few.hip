@@ -16,7 +16,8 @@
 // columns, so what a step takes adds up: products alone 9.2 us, reading and filling
 // LDS 5 to 8, launch, first loads and last sums 4.4.  Not faster: loads through
 // registers (24.0), operands fetched a half step ahead and spread among the products
-// (26), other first columns for every block (21.5, and 3 more for few rows).
+// (26), other first columns for every block (21.5, and 3 more for few rows), two
+// waves a SIMD that take turns at reading and multiplying (26).
 #include <hip/hip_runtime.h>
 
 #include "step.h"
