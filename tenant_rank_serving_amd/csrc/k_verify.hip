@@ -119,10 +119,10 @@ __device__ __forceinline__ void keep_larger(float& m, int& at, float m2, int at2
 }
 
 // ------------------------------------------------------------------ stats
-// Block (piece, row, side).  Bound by the vector unit, whose 28 instructions for a
-// logit are 18 fp64 ones of the exponential, its conversion, the maximum and the
-// test for NaN, and for fp32 logits by HBM almost as much: 455 rows of 100003 fp32
-// logits 43 us (4.2 TB/s), 829 rows of bf16 67 us (2.5 TB/s).
+// Block (piece, row, side).  Bound by the vector unit, whose 22 instructions for a
+// logit are 18 fp64 ones of the exponential, the maximum, the test for NaN and the
+// reductions' share, and for fp32 logits by HBM almost as much: 455 rows of 100003
+// fp32 logits 43 us (4.2 TB/s), 829 rows of bf16 67 us (2.5 TB/s).
 template <bool F32, int U>
 __global__ void __launch_bounds__(kThreads) k_verify_stats(VerifyArgs a) {
   __shared__ float sm[4];
