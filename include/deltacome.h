@@ -815,9 +815,9 @@ dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32
  * in a fixed order: the tokens are those of the formula wherever its two sides
  * differ by more than about 1e-13 of the sum.
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_BUFFER,
- * DC_ERR_UNSUPPORTED (a vocabulary of more than 2^30, 2^24 pieces of 8192
- * logits or more, or rows that lie
- * beyond 2^47 bytes).
+ * DC_ERR_UNSUPPORTED (a vocabulary of more than 2^30; 2^24 pieces of 8192
+ * logits or more in the rows of target and draft, or 2^22 in one row of each
+ * sequence; rows that lie beyond 2^47 bytes).
  */
 enum { DC_LOGITS_BF16 = 0, DC_LOGITS_F32 = 1 };
 

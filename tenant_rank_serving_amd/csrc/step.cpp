@@ -60,7 +60,8 @@ bool overlap(const Span (&w)[W], const Span (&r)[R]) {
 bool verify_size(int32_t vocab, int32_t N, int32_t seqs) {
   if (vocab < 1 || N < 0 || seqs < 0) return false;
   const int64_t most = ((int64_t)vocab + 14) / 8 / (4 * kVerifyThreads) + 1;
-  return mul_fits(most, 2 * (int64_t)N, kMostBlocks - 1) && mul_fits(most, seqs, kMostBlocks - 1) && vocab <= (1 << 30);
+  // (a sequence has a block of 512 threads for 4096 logits, or one of up to 1024 threads)
+  return mul_fits(most, 2 * (int64_t)N, kMostBlocks - 1) && mul_fits(most, seqs, (kMostBlocks - 1) / 4) && vocab <= (1 << 30);
 }
 
 dc_status check_table(const dc_kv_table* t, uint32_t* status, void* stream, TableArgs* a) {

@@ -170,6 +170,38 @@ def test_verify_masks_and_rows_without_a_distribution():
     v.check()
 
 
+@pytest.mark.parametrize("nq,vocab,dtype,draft", [
+    ([1], 150001, "bf16", False), ([2, 1], 150001, "f32", True), ([3] * 5, 300001, "bf16", True), ([1, 2, 2, 3], 600007, "f32", False)])
+def test_verify_many_pieces(nq, vocab, dtype, draft):
+    """More pieces of a row than lanes of a wave, of each of the sizes."""
+    note("verify, many pieces", nq, vocab, dtype, draft)
+    for seed in (1, 2, 3):
+        Verify(seed, nq, vocab, dtype, draft, "hot", hot=0.0).check()
+
+
+@pytest.mark.parametrize("b,vocab,dtype", [(6, 5003, "bf16"), (6, 5003, "f32"), (64, 70001, "bf16"), (64, 70001, "f32")])
+def test_verify_looked_up_drafts_of_likely_tokens(b, vocab, dtype):
+    """Drafts without logits that have nearly all or all of the probability and fall: the rest of the row, or the draft."""
+    note("verify, likely", b, vocab, dtype)
+    v = Verify(b, [2] * b, vocab, dtype, False, "hot")
+    rng = np.random.default_rng(b)
+    v.accept[:] = np.nan                                     # no draft stands
+    rows = np.arange(0, 2 * b, 2)
+    at = rng.integers(0, vocab, b)
+    at[:4] = [0, vocab - 1, 2047, 4096]
+    v.tokens[rows + 1] = at
+    lift = np.resize([0.0, 12.0, 24.0, 40.0], b)             # 40 T: the rest has 1e-13 of it
+    v.x[rows, at] = 12.0 + lift
+    alone = rows[4::5]
+    v.x[alone] = -np.inf                                     # nothing is left
+    v.x[alone, at[4::5]] = 1.0
+    if dtype == "bf16":
+        v.x = vals(bits(v.x))
+    v.check()
+    out = v.out.cpu().numpy()
+    assert (out[alone] == at[4::5]).all() and (np.delete(out[rows], np.s_[4::5]) != np.delete(at, np.s_[4::5])).all()
+
+
 def test_verify_greedy_ties_and_masks():
     note("verify, greedy")
     v = Verify(4, [3] * 6, 9001, "f32", True, "hot")

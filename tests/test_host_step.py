@@ -59,6 +59,14 @@ def test_verify_refusals(L, kw, want):
     assert verify(L, **kw) == want
 
 
+def test_verify_most_sequences(L):
+    """Launches have fewer than 2^32 threads: up to 4 per 32 logits of a sequence's row, 1024 at least."""
+    size = L.dc_verify_workspace_bytes
+    assert size(10, 9, (1 << 22) - 1) > 0 and size(10, 9, 1 << 22) == 0
+    assert size(100003, 9, (1 << 22) // 13) > 0 and size(100003, 9, (1 << 22) // 13 + 1) == 0
+    assert verify(L, batch(seqs=1 << 22)) == E.DC_ERR_UNSUPPORTED
+
+
 def test_verify_workspace(L):
     size = L.dc_verify_workspace_bytes
     assert size(1000, 9, 3) % 256 == 0 and size(1000, 9, 3) >= 9 * 2 * 16 + 3 * 20
