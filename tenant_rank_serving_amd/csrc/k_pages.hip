@@ -17,8 +17,13 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 // ------------------------------------------------------------------ tables
 constexpr int kResizeThreads = 1024, kWaves = kResizeThreads / 64;
 
-__device__ __forceinline__ int32_t ld_agent(const int32_t* p) {
-  return __hip_atomic_load(const_cast<int32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// The counts of k_resize are one block's alone while it runs, so its atomics need
+// not leave the XCD's L2.
+__device__ __forceinline__ int32_t ld_block(const int32_t* p) {
+  return __hip_atomic_load(const_cast<int32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+__device__ __forceinline__ void add_block(int32_t* p, int32_t v) {
+  __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 __device__ __forceinline__ void add_agent(int32_t* p, int32_t v) {
   __hip_atomic_fetch_add(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -58,36 +63,57 @@ __device__ __forceinline__ int upto_lane(int v) {
 //
 // Bound by latency: lengths, entries, counts and free pages are read one after
 // the other, about a microsecond each.  48 of 64 sequences giving back 5000 pages
-// (whose counts one CU's path to the L2 takes one by one) 12 us, growing by 255
-// pages out of 6100 9 us.
+// 7 us, growing by 255 pages out of 6100 7 us.
 __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const int32_t* new_len, int32_t* copies) {
   // per sequence: pages needed up to and with it, and whether the first of its own is for an exchange;
-  // its old length
-  __shared__ uint32_t upto[DC_KV_MAX_SEQS];
-  __shared__ int32_t old_of[DC_KV_MAX_SEQS];
+  // its old length.  Before that, per page: how often it is given back
+  constexpr int kCounted = 2 * DC_KV_MAX_SEQS;
+  __shared__ union {
+    struct {
+      uint32_t upto[DC_KV_MAX_SEQS];
+      int32_t old_of[DC_KV_MAX_SEQS];
+    };
+    alignas(16) int32_t freed[kCounted];
+  } sh;
+  uint32_t* upto = sh.upto;
+  int32_t* old_of = sh.old_of;
   __shared__ int32_t given[kResizeThreads];   // what the first sequences get for their shared pages
+  __shared__ int32_t list[4 * kResizeThreads];   // free pages, in order
   __shared__ int box[kWaves];
   __shared__ uint32_t status;
+  __shared__ int giving;   // sequences that give pages back, 64 for one with 64
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int most = t.width * t.page, shift = 31 - __builtin_clz(t.page);
   auto pages_of = [&](int n) { return (int)(((int64_t)n + t.page - 1) >> shift); };
-  if (tid == 0) status = 0;
+  if (tid == 0) status = 0, giving = 0;
   __syncthreads();
 
-  // the first kResizeThreads sequences' lengths and shared pages, for later
-  int old0 = 0, want0 = 0;
-  int32_t shared0 = -1;
-  if (tid < t.seqs) {
-    old0 = t.kv_len[tid], want0 = new_len[tid];
-    if (old0 >= 0 && old0 < want0 && want0 <= most && (old0 & (t.page - 1))) shared0 = t.pages[(int64_t)tid * t.width + (old0 >> shift)];
+  // the first kResizeThreads sequences' lengths, in the order in which the waves
+  // take them now and in the one of later
+  int old1 = 0, want1 = 0, old0 = 0, want0 = 0;
+  if (wave + lane * kWaves < t.seqs) old1 = t.kv_len[wave + lane * kWaves], want1 = new_len[wave + lane * kWaves];
+  if (tid < t.seqs) old0 = t.kv_len[tid], want0 = new_len[tid];
+  const int give = old1 <= most && want1 >= 0 ? pages_of(old1) - pages_of(want1) : 0;
+  // Many pages are counted in LDS and their counts fall once: one CU's atomics on
+  // the L2 take 1.7 ns each (5000: 8.7 us, this way 3).  A few would not pay for it.
+  const uint64_t some = __ballot(give >= 2), lots = __ballot(give >= 64);
+  if (lane == 0 && some) atomicAdd(&giving, lots ? 64 : __builtin_popcountll(some));
+  __syncthreads();
+  const bool many = t.num_pages <= kCounted && giving >= 64;
+  if (many) {
+    for (int i = tid; i < (t.num_pages + 3) / 4; i += kResizeThreads) reinterpret_cast<int4*>(sh.freed)[i] = int4{0, 0, 0, 0};
+    __syncthreads();
   }
+  int32_t shared0 = -1;
+  if (tid < t.seqs && old0 >= 0 && old0 < want0 && want0 <= most && (old0 & (t.page - 1)))
+    shared0 = t.pages[(int64_t)tid * t.width + (old0 >> shift)];
   // 64 sequences of a wave at a time, a length in each lane; then those that give
   // pages back, 256 entries of one at a time, with the next ones' on their way
   for (int s0 = wave; s0 < t.seqs; s0 += 64 * kWaves) {
     const int b = s0 + lane * kWaves;
     int from = 0, to = 0;
     if (b < t.seqs) {
-      const int old = t.kv_len[b], want = new_len[b];
+      const int old = s0 == wave ? old1 : t.kv_len[b], want = s0 == wave ? want1 : new_len[b];
       if (old < 0 || old > most || want < 0 || want > most) atomicOr(&status, (uint32_t)DC_KV_BAD);
       else from = pages_of(want), to = pages_of(old);
     }
@@ -114,8 +140,9 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
       for (int j = 0; j < 4; ++j) {
         const int i = at_ + 64 * j + lane;
         if (i >= end_) continue;
-        if (e[j] >= 0 && e[j] < t.num_pages) add_agent(t.refs + e[j], -1);
-        else atomicOr(&status, (uint32_t)DC_KV_BAD);
+        if (e[j] < 0 || e[j] >= t.num_pages) atomicOr(&status, (uint32_t)DC_KV_BAD);
+        else if (many) atomicAdd(&sh.freed[e[j]], 1);
+        else add_block(t.refs + e[j], -1);
         row[i] = -1;
       }
       if (!todo) break;
@@ -125,9 +152,24 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   }
   __builtin_amdgcn_s_waitcnt(0);   // the counts have fallen
   __syncthreads();
+  const int vecs = (t.num_pages + 3) / 4;
+  if (many) {
+    for (int v = tid; v < vecs; v += kResizeThreads) {
+      const int4 n = reinterpret_cast<const int4*>(sh.freed)[v];
+      if (!(n.x | n.y | n.z | n.w)) continue;
+      if (4 * v + 3 < t.num_pages) {
+        int4 r = reinterpret_cast<const int4*>(t.refs)[v];
+        r.x -= n.x, r.y -= n.y, r.z -= n.z, r.w -= n.w;
+        reinterpret_cast<int4*>(t.refs)[v] = r;
+      } else {
+        for (int i = 4 * v; i < t.num_pages; ++i) t.refs[i] -= sh.freed[i];
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+  }
 
   // the free pages: 4 a thread, the next ones on their way while these are dealt
-  const int vecs = (t.num_pages + 3) / 4;
   auto load = [&](int v) {
     int4 r = int4{1, 1, 1, 1};
     if (4 * v + 3 < t.num_pages) r = reinterpret_cast<const int4*>(t.refs)[v];
@@ -138,8 +180,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
     }
     return r;
   };
-  // (the counts that fell are in the L2; nothing of them is in this CU's L1 yet)
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  // (counts that fell by atomics are in the L2; nothing of them is in this CU's L1 yet)
   int4 now = load(tid), next = load(kResizeThreads + tid);
 
   int total = 0;
@@ -154,7 +195,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
         need = pages_of(want) - pages_of(old);
         if (old & (t.page - 1)) {
           const int32_t p = b0 ? t.pages[(int64_t)b * t.width + (old >> shift)] : shared0;
-          if (p >= 0 && p < t.num_pages) swap = ld_agent(t.refs + p) > 1;
+          if (p >= 0 && p < t.num_pages) swap = ld_block(t.refs + p) > 1;
           else atomicOr(&status, (uint32_t)DC_KV_BAD);
           need += swap;
         }
@@ -178,35 +219,36 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
     for (int j = 0; j < 4; ++j) mine += r[j] <= 0;
     const int sum = upto_lane(mine);
     int all;
-    int k = dealt + before_wave(__shfl(sum, 63), box, &all) + sum - mine;
+    int at = before_wave(__shfl(sum, 63), box, &all) + sum - mine;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (r[j] > 0) continue;
-      if (k < total) {
-        const int32_t p = 4 * (v0 + tid) + j;
-        int lo = 0, hi = t.seqs - 1;   // the first sequence with upto > k
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if ((int)(upto[mid] >> 1) > k) hi = mid; else lo = mid + 1;
-        }
-        const int slot = k - (lo ? (int)(upto[lo - 1] >> 1) : 0);
-        const bool swap = upto[lo] & 1;
-        const int old = old_of[lo];
-        int32_t* row = t.pages + (int64_t)lo * t.width;
-        if (swap && slot == 0) {
-          if (lo < kResizeThreads) {
-            given[lo] = p;
-          } else {
-            copies[2 * lo] = row[old >> shift];
-            copies[2 * lo + 1] = p;
-            row[old >> shift] = p;
-          }
-        } else {
-          row[pages_of(old) + slot - swap] = p;
-        }
-        t.refs[p] = 1;
+    for (int j = 0; j < 4; ++j)
+      if (r[j] <= 0) list[at++] = 4 * (v0 + tid) + j;
+    __syncthreads();
+    const int deal = min(all, total - dealt);
+    for (int i = tid; i < deal; i += kResizeThreads) {
+      const int32_t p = list[i];
+      const int k = dealt + i;
+      int lo = 0, hi = t.seqs - 1;   // the first sequence with upto > k
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int)(upto[mid] >> 1) > k) hi = mid; else lo = mid + 1;
       }
-      ++k;
+      const int slot = k - (lo ? (int)(upto[lo - 1] >> 1) : 0);
+      const bool swap = upto[lo] & 1;
+      const int old = old_of[lo];
+      int32_t* row = t.pages + (int64_t)lo * t.width;
+      if (swap && slot == 0) {
+        if (lo < kResizeThreads) {
+          given[lo] = p;
+        } else {
+          copies[2 * lo] = row[old >> shift];
+          copies[2 * lo + 1] = p;
+          row[old >> shift] = p;
+        }
+      } else {
+        row[pages_of(old) + slot - swap] = p;
+      }
+      t.refs[p] = 1;
     }
     dealt += all;
     now = next;
@@ -249,7 +291,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
         copies[2 * b + 1] = given[tid];
         t.pages[(int64_t)b * t.width + (old >> shift)] = given[tid];
       }
-      add_agent(t.refs + (b0 ? copies[2 * b] : shared0), -1);
+      add_block(t.refs + (b0 ? copies[2 * b] : shared0), -1);
     }
     t.kv_len[b] = want;
   }

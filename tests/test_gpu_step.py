@@ -377,6 +377,13 @@ def test_tables_walk(seqs, width, page, num_pages, held, seed):
     assert (t.lens == 0).all() and (t.pages == -1).all()
 
 
+@pytest.mark.parametrize("seqs,width,page,num_pages,held,seed", [
+    (40, 200, 16, 32767, 9000, 7), (40, 200, 16, 32768, 28000, 8), (40, 200, 16, 32770, 9000, 9), (1100, 3, 32, 2501, 3, 10)])
+def test_tables_give_back_many(seqs, width, page, num_pages, held, seed):
+    """Long sequences closed in great numbers, in pools around the size up to which their pages are counted first."""
+    test_tables_walk(seqs, width, page, num_pages, held, seed)
+
+
 def test_tables_running_out():
     note("tables, running out")
     t = Table([[2, 5, -1, -1], [2, 5, -1, -1], [-1] * 4, [7, -1, -1, -1]], [20, 20, 0, 16], [1, 0, 2, 1, 1, 2, 0, 1, 0], 16)
