@@ -130,8 +130,8 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(VerifyArgs a) {
   __shared__ double sz[4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int sides = a.q ? 2 : 1, c = blockIdx.x % a.chunks, rs = blockIdx.x / a.chunks, side = rs % sides, row = rs / sides;
-  // the counters of the next launch
-  for (int i = blockIdx.x * kThreads + tid; i < a.seqs; i += gridDim.x * kThreads) a.arrived[i] = 0;
+  // the counters of the next launch (the grid's threads are numbered with 32 bits: a step further needs more)
+  for (size_t i = (size_t)blockIdx.x * kThreads + tid; i < (size_t)a.seqs; i += (size_t)gridDim.x * kThreads) a.arrived[i] = 0;
   const int V = a.vocab;
   const void* l = side ? row_of<F32>(a.q, a.qs, row) : row_of<F32>(a.p, a.ps, row);
   const int lead = lead_of<F32>(l);

@@ -294,6 +294,30 @@ def test_verify_captured_two_sizes_share_a_workspace():
         b.compare()
 
 
+def test_verify_more_blocks_than_31_bits_of_threads():
+    """Rows whose statistics take more than 2^31 threads: the counters that they clear on the way are those of the
+    sequences, whatever a block's number."""
+    t = torch()
+    n, b, vocab = 4300000, 1000, 2
+    note("verify, many rows", n, b, vocab)
+    rng = np.random.default_rng(13)
+    x, y = (t.from_numpy(rng.normal(size=(n, vocab)).astype(np.float32)).cuda().bfloat16() for _ in range(2))
+    q_start = (np.arange(b + 1) * (n // b)).astype(np.int32)
+    tokens, picks = rng.integers(0, vocab, n).astype(np.int32), rng.random(b).astype(np.float32)
+    accept = t.full((n,), float("nan"), device="cuda")       # no draft stands
+    batch = trs.VerifyBatch(dev_i32(q_start), dev_i32(tokens), accept, dev_f32(picks))
+    ws = t.full((trs.dc_verify_workspace_bytes(vocab, n, b),), 0xA5, dtype=t.uint8, device="cuda")
+    out, count = t.zeros(n, dtype=t.int32, device="cuda"), t.zeros(b, dtype=t.int32, device="cuda")
+    trs.dc_verify_drafts(batch, x, y, out, count, ws)
+    t.cuda.synchronize()
+    rows = (q_start[:-1, None] + np.arange(2)).reshape(-1)   # a sequence's first row and its draft decide
+    px, py = (a[t.from_numpy(rows).cuda().long()].double().cpu().numpy() for a in (x, y))
+    want, _, _, margin = step.verify(px, py, np.arange(0, 2 * b + 1, 2), tokens[rows], np.full(2 * b, np.nan), picks, None)
+    assert margin > 1e-11
+    got = out.cpu().numpy().reshape(b, -1)
+    assert got[:, 0].tolist() == want[::2] and (got[:, 1:] == -1).all() and (count == 1).all()
+
+
 def test_verify_binding_refusals():
     t = torch()
     v = Verify(12, [2, 2], 64, "f32", True).upload()
