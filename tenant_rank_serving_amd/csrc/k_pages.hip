@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   }
   __builtin_amdgcn_s_waitcnt(0);   // the counts have fallen
   __syncthreads();
-  const int vecs = (t.num_pages + 3) / 4;
+  const int vecs = (int)(((int64_t)t.num_pages + 3) / 4);
   if (many) {
     for (int v = tid; v < vecs; v += kResizeThreads) {
       const int4 n = reinterpret_cast<const int4*>(sh.freed)[v];
@@ -172,12 +172,12 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   // the free pages: 4 a thread, the next ones on their way while these are dealt
   auto load = [&](int v) {
     int4 r = int4{1, 1, 1, 1};
-    if (4 * v + 3 < t.num_pages) r = reinterpret_cast<const int4*>(t.refs)[v];
-    else if (v < vecs) {
-      r.x = t.refs[4 * v];
-      if (4 * v + 1 < t.num_pages) r.y = t.refs[4 * v + 1];
-      if (4 * v + 2 < t.num_pages) r.z = t.refs[4 * v + 2];
-    }
+    if (v >= vecs) return r;   // (4 v may have 32 bits from here on)
+    const unsigned p = 4u * (unsigned)v, pages = (unsigned)t.num_pages;
+    if (p + 3 < pages) return reinterpret_cast<const int4*>(t.refs)[v];
+    r.x = t.refs[p];
+    if (p + 1 < pages) r.y = t.refs[p + 1];
+    if (p + 2 < pages) r.z = t.refs[p + 2];
     return r;
   };
   // (counts that fell by atomics are in the L2; nothing of them is in this CU's L1 yet)

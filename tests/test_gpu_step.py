@@ -486,6 +486,23 @@ def test_tables_many_sequences():
     a.resize(rng.integers(0, 49, 16384))
 
 
+def test_tables_of_nearly_2_to_the_31_pages():
+    """The most pages that 31 bits number, all held but a few at either end: what is read ahead ends with the counts."""
+    t = torch()
+    num = 2 ** 31 - 1
+    note("tables, pages", num)
+    refs = t.ones(num, dtype=t.int32, device="cuda")
+    refs[5], refs[num - 3:] = 0, 0
+    pages, lens = t.full((3, 4), -1, dtype=t.int32, device="cuda"), t.zeros(3, dtype=t.int32, device="cuda")
+    table, status = trs.KvTable(pages, lens, refs, 16), t.zeros(1, dtype=t.int32, device="cuda")
+    copies = t.zeros(3, 2, dtype=t.int32, device="cuda")
+    trs.dc_kv_resize(table, dev_i32([20, 16, 30]), copies, status)
+    assert pages[:, 0].tolist() == [5, num - 2, -1] and pages[0, 1].item() == num - 3 and lens.tolist() == [20, 16, 0]
+    assert refs[num - 3:].tolist() == [1, 1, 0] and refs[5].item() == 1 and status.item() == trs.DC_KV_FULL
+    trs.dc_kv_resize(table, dev_i32([0, 0, 64]), copies, status)
+    assert pages.tolist() == [[-1] * 4, [-1] * 4, [5, num - 3, num - 2, num - 1]] and lens.tolist() == [0, 0, 64]
+
+
 # ------------------------------------------------------------------ pages
 class Layers:
     """Pools of `layers` layers, every slot different: [layer] of [pages][heads][page][dim] codes on the host."""
