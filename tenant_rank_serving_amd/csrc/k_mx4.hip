@@ -265,18 +265,19 @@ int launch_mx4q(const Mx4Args& a) {
   return (int)hipGetLastError();
 }
 
+// Pieces of 64 rows and 512 columns (columns: up to 2^31 less 128).
+static unsigned pieces_of(int32_t rows, int32_t cols) { return ((unsigned)rows + 63) / 64 * (((unsigned)cols + 511) / 512); }
+
 int launch_mx4_pack(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, uint8_t* dst, uint32_t* flag,
                     void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (flag) hipLaunchKernelGGL(k_mx4_flag, dim3(1), dim3(1), 0, st, flag);
-  const unsigned g = (unsigned)((rows + 63) / 64) * (unsigned)((cols + 511) / 512);
-  hipLaunchKernelGGL(k_mx4_pack, dim3(g), dim3(256), 0, st, X, stride, dst, flag, rows, cols);
+  hipLaunchKernelGGL(k_mx4_pack, dim3(pieces_of(rows, cols)), dim3(256), 0, st, X, stride, dst, flag, rows, cols);
   return (int)hipGetLastError();
 }
 
 int launch_mx4_dequant(int32_t rows, int32_t cols, const uint8_t* w, uint16_t* X, int64_t stride, void* stream) {
-  const unsigned g = (unsigned)((rows + 63) / 64) * (unsigned)((cols + 511) / 512);
-  hipLaunchKernelGGL(k_mx4_dequant, dim3(g), dim3(256), 0, reinterpret_cast<hipStream_t>(stream), w, X, stride, rows, cols);
+  hipLaunchKernelGGL(k_mx4_dequant, dim3(pieces_of(rows, cols)), dim3(256), 0, reinterpret_cast<hipStream_t>(stream), w, X, stride, rows, cols);
   return (int)hipGetLastError();
 }
 

@@ -241,7 +241,7 @@ dc_status dc_kv_compact(const dc_kv_cache* layers, int32_t n_layers, const int32
 
 size_t dc_mx4_bytes(int32_t rows, int32_t cols) {
   if (rows < 1 || cols < 1 || cols % 128) return 0;
-  return mx4_codes(rows, cols) + (size_t)((rows + 15) / 16) * (size_t)((cols + 511) / 512) * 256;
+  return mx4_codes(rows, cols) + ((size_t)rows + 15) / 16 * (((size_t)cols + 511) / 512) * 256;
 }
 
 dc_status dc_mx4_pack_device(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, void* dst, size_t dst_bytes,

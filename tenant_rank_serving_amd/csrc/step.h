@@ -74,7 +74,7 @@ struct Mx4Args {
   void* stream;
 };
 // Bytes of the codes of a matrix.
-inline size_t mx4_codes(int32_t rows, int32_t cols) { return (size_t)((rows + 15) / 16) * 16 * (size_t)cols / 2; }
+inline size_t mx4_codes(int32_t rows, int32_t cols) { return ((size_t)rows + 15) / 16 * 16 * (size_t)cols / 2; }
 int launch_mx4(const Mx4Args& a);
 int launch_mx4_few(const Mx4Args& a);   // of it, more than 16 tokens
 int launch_mx4q(const Mx4Args& a);

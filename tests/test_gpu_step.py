@@ -662,6 +662,24 @@ def test_mx4_pack(rows, cols, stride):
     assert np.array_equal(host_bits(back2[:, :cols]), host_bits(back[:, :cols]))
 
 
+def test_mx4_pack_of_the_longest_rows():
+    """One row of as many columns as 31 bits hold, 512 of them over and over; the last ones are 384."""
+    t = torch()
+    cols = 2 ** 31 - 128
+    note("mx4 pack, longest row", cols)
+    part = bits(np.random.default_rng(2).normal(size=(1, 512)))
+    x = dev_bits(part)[0].repeat(2 ** 22)[:cols].view(1, cols)
+    view, flag = mx4_empty(1, cols), t.ones(1, dtype=t.int32, device="cuda")
+    trs.dc_mx4_pack_device(x, view, flag)
+    one = step.mx4_pack(*step.mx4_quantize(vals(part)))
+    codes, words = t.from_numpy(one[:4096]).cuda().view(t.int64), t.from_numpy(one[4096:].copy()).cuda().view(t.int32)
+    n = cols * 8
+    got, scales = view.buf[:n].view(t.int64), view.buf[n:].view(t.int32)
+    assert flag.item() == 0 and scales.numel() == 64 * 2 ** 22
+    assert bool((got[:512 * (2 ** 22 - 1)].view(-1, 512) == codes).all()) and t.equal(got[512 * (2 ** 22 - 1):], codes[:384])
+    assert bool((scales[:-64].view(-1, 64) == words).all()) and t.equal(scales[-64:], words & 0xFFFFFF)
+
+
 def test_mx4_pack_every_bit_pattern():
     """Every bf16 number as the largest of a block and beside a larger one; infinities and NaN make a block NaN."""
     t = torch()

@@ -217,6 +217,18 @@ def test_mx4_bytes():
     assert trs.dc_mx4_bytes(1 << 20, 1 << 20) == (1 << 39) + (1 << 35)
 
 
+def test_mx4_bytes_at_the_ends_of_its_arguments(L):
+    """Rows and columns up to the last ones that 31 bits hold, in exact arithmetic."""
+    up = lambda a, b: -(-a // b)  # noqa: E731
+    for rows in (1, 16, 17, 1 << 30, INT_MAX - 15, INT_MAX - 14, INT_MAX):
+        for cols in (128, 512, 640, 1 << 30, 2 ** 31 - 640, 2 ** 31 - 512, 2 ** 31 - 384, 2 ** 31 - 128):
+            want = up(rows, 16) * 16 * cols // 2 + up(rows, 16) * up(cols, 512) * 256
+            assert trs.dc_mx4_bytes(rows, cols) == want, (rows, cols)
+    # a buffer one byte short of such a row is refused
+    cols = 2 ** 31 - 128
+    assert pack(L, rows=1, cols=cols, stride=cols, x=1 << 40, dst=1 << 44, n=trs.dc_mx4_bytes(1, cols) - 1) == E.DC_ERR_BUFFER
+
+
 def test_mx4_refusals(L):
     assert apply(L) == E.DC_OK and pack(L, rows=0) == E.DC_OK and pack(L, rows=0, n=0, flag=None) == E.DC_OK
     size = trs.dc_mx4_bytes(256, 384)
