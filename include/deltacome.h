@@ -900,8 +900,9 @@ dc_status dc_kv_fork(const dc_kv_table* t, const int32_t* src, const int32_t* ds
  * (those of dc_kv_resize that need no copy).  A page that is `to` must not be in
  * any other pair (of two writes either's pieces may be found there).
  *   layers  host array [n_layers] of caches that differ in k, v (and scales)
- *           only, 1 .. DC_KV_MAX_LAYERS; no two may overlap
- *   copies  device int32 [n][2]
+ *           only, 1 .. DC_KV_MAX_LAYERS; no two may overlap, nor keys and
+ *           values (not checked)
+ *   copies  device int32 [n][2]; must not lie in a layer's pages
  * Errors as for dc_kv_append's cache; DC_ERR_SHAPE if the caches differ,
  * DC_ERR_UNSUPPORTED (more layers, or more than 2^24 blocks of 16 KiB).
  */
@@ -920,6 +921,7 @@ dc_status dc_kv_copy(const dc_kv_cache* layers, int32_t n_layers, const int32_t*
  *             `from`, nor with each other; or NULL: in place.  In place a
  *             sequence's positions must ascend, and its pages be held by it
  *             alone (as far as they are written)
+ * None of them may lie in a layer's pages.
  * Positions and pages out of range are left out.  Errors as for dc_kv_copy
  * (2^24 blocks of 64 tokens and 4 heads, or of a sequence in place).
  */

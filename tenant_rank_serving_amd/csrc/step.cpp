@@ -105,6 +105,23 @@ dc_status check_layers(const dc_kv_cache* c, int32_t n, LayerArgs* a) {
   return DC_OK;
 }
 
+// Whether n bytes at p reach into a page of some layer.
+bool in_layers(const LayerArgs& a, const void* p, int64_t n) {
+  KvArgs k{};
+  k.page_stride = a.page_stride;
+  k.head_stride = a.head_stride;
+  k.slot_stride = a.slot_stride;
+  k.heads = a.heads;
+  k.num_pages = a.num_pages;
+  k.shift = a.shift;
+  for (int32_t i = 0; i < a.layers; ++i) {
+    k.k = a.k[i];
+    k.v = a.v[i];
+    if (in_cache(k, INT64_C(16) << a.pieces, p, n)) return true;
+  }
+  return false;
+}
+
 dc_status check_mx4(const dc_mx4_view* w) {
   if (!w) return DC_ERR_INVALID_ARG;
   if (dc_mx4_bytes(w->rows, w->cols) == 0) return DC_ERR_SHAPE;
@@ -219,6 +236,7 @@ dc_status dc_kv_copy(const dc_kv_cache* layers, int32_t n_layers, const int32_t*
   const int64_t pieces = ((int64_t)a.heads << a.shift) << a.pieces, parts = (pieces + kCopyBlock - 1) / kCopyBlock;
   if (pieces > INT32_MAX / 2 || parts > 65535 || !mul_fits(2 * (int64_t)n_layers * parts, n, kMostBlocks)) return DC_ERR_UNSUPPORTED;
   if (n == 0) return DC_OK;
+  if (in_layers(a, copies, 8 * (int64_t)n)) return DC_ERR_INVALID_ARG;
   return launch_copy(a, copies, n, stream) == 0 ? DC_OK : DC_ERR_HIP;
 }
 
@@ -236,6 +254,10 @@ dc_status dc_kv_compact(const dc_kv_cache* layers, int32_t n_layers, const int32
   if (!from || !keep_start || !keep) return DC_ERR_INVALID_ARG;
   if (!aligned(from, 4) || !aligned(keep_start, 4) || !aligned(keep, 4) || !aligned(to, 4)) return DC_ERR_ALIGN;
   if (from == to) return DC_ERR_INVALID_ARG;   // in place is to = NULL
+  const int64_t table = 4 * (int64_t)seqs * width;
+  if (in_layers(a, from, table) || (to && in_layers(a, to, table)) || in_layers(a, keep_start, 4 * (int64_t)seqs + 4) ||
+      in_layers(a, keep, 4 * (int64_t)n))
+    return DC_ERR_INVALID_ARG;
   return launch_compact(a, from, to, keep_start, keep, seqs, width, n, stream) == 0 ? DC_OK : DC_ERR_HIP;
 }
 

@@ -186,6 +186,25 @@ def test_page_refusals(L):
         assert compact(L, **kw) == want, kw
 
 
+def test_what_the_pages_hold_is_not_what_a_call_reads(L):
+    """Pairs, tables and positions that lie in a page of any layer's keys or values; room between pages is none of them."""
+    size = 10 * 4 * 16 * 128 * 2
+    pools = (0x10000, 0x4000000, 0x8000000, 0x9000000)          # keys and values of the two layers
+    for p in pools:
+        for at in (p - 4, p, p + size - 8):
+            assert copy(L, n=1, copies=at) == E.DC_ERR_INVALID_ARG, hex(at)
+            for kw in (dict(source=at), dict(to=at), dict(start=at), dict(keep=at, n=2)):
+                assert compact(L, **{**dict(n=1), **kw}) == E.DC_ERR_INVALID_ARG, (hex(at), kw)
+                if "to" not in kw:
+                    assert compact(L, **{**dict(n=1, to=None), **kw}) == E.DC_ERR_INVALID_ARG, (hex(at), kw)
+    # pages 128 elements further apart than they are long, the last one's end
+    wide = layers(dict(page_stride=4 * 16 * 128 + 128))
+    page = 4 * 16 * 128 * 2
+    for at, want in ((0x10000 + page - 4, E.DC_ERR_INVALID_ARG), (0x10000 + page + 252, E.DC_ERR_INVALID_ARG),
+                     (0x10000 + 9 * (page + 256) + page - 4, E.DC_ERR_INVALID_ARG)):
+        assert copy(L, wide, n=1, copies=at) == want, hex(at)
+
+
 INT_MAX = 2 ** 31 - 1
 
 
