@@ -810,7 +810,8 @@ dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32
  *                (>= vocab; any alignment of whole elements).  draft's row of a
  *                sequence's last row is not read
  *   ws           ws_bytes >= dc_verify_workspace_bytes(vocab, N, seqs), 256-byte
- *                aligned; holds nothing between calls
+ *                aligned; holds nothing between calls.  The size falls with none
+ *                of the three: the largest call's workspace serves smaller ones
  * Arithmetic: weights, sums and comparisons in fp64 (the exponentials to 2e-14),
  * in a fixed order: the tokens are those of the formula wherever its two sides
  * differ by more than about 1e-13 of the sum.

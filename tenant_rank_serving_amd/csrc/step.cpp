@@ -26,7 +26,12 @@ VerifyPlan verify_plan(int32_t vocab, int32_t N, int32_t seqs) {
   p.pieces = (int32_t)chunks(pick_threads(p.vecs) / kVerifyThreads);
   p.rest_off = round_up(sizeof(VerifyPart) * 2 * (size_t)N * p.chunks, kAlign);
   p.arrived_off = p.rest_off + round_up(2 * sizeof(double) * (size_t)seqs * p.pieces, kAlign);
-  p.ws = p.arrived_off + round_up(4 * (size_t)seqs, kAlign);
+  // What a call needs falls where longer pieces begin.  A workspace serves smaller
+  // calls too, so its size is a bound that grows with each argument: short pieces
+  // are taken while chunks(4) * N is 511 or less, when there are at most 4 * 511.
+  const int64_t shorts = std::min<int64_t>(chunks(1) * N, 4 * 511), longs = chunks(4) * N;
+  p.ws = round_up(sizeof(VerifyPart) * 2 * (size_t)std::max(shorts, longs), kAlign) +
+         round_up(2 * sizeof(double) * (size_t)(chunks(1) * seqs), kAlign) + round_up(4 * (size_t)seqs, kAlign);
   return p;
 }
 

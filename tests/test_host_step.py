@@ -76,6 +76,30 @@ def test_verify_workspace(L):
     assert verify(L, nws=need - 1) == E.DC_ERR_BUFFER
 
 
+def test_verify_workspace_of_a_larger_call_serves_a_smaller(L):
+    """The size falls with none of its arguments, pieces of either length among them; calls are looked at up to the check
+    behind the workspace's (an output in the logits)."""
+    size = L.dc_verify_workspace_bytes
+    for vocab in (1, 50, 2034, 2035, 8178, 8179, 32000, 100003, 128256, 1 << 22, 1 << 30):
+        for seqs in (0, 1, 64, 3000):
+            if seqs * (vocab // 8192 + 2) >= 1 << 22:
+                continue
+            all_n = sorted({n for n in [*range(0, 700), 1023, 1024, 4000, 65536] if 2 * n * (vocab // 8192 + 2) < 1 << 24})
+            sizes = [size(vocab, n, seqs) for n in all_n]
+            assert sizes == sorted(sizes) and sizes[0] > 0, (vocab, seqs)
+    for n in (1, 2, 31, 32, 33, 40, 127, 128, 129, 255, 256, 257, 511, 512, 513, 2000):
+        for seqs in (1, n):
+            sizes = [size(v, n, seqs) for v in range(1, 140000, 97)]
+            assert sizes == sorted(sizes), (n, seqs)
+    for n in (1, 127, 128, 600):
+        sizes = [size(32000, n, s) for s in range(0, 2000)]
+        assert sizes == sorted(sizes), n
+    for vocab, most in ((32000, 128), (32000, 200), (100003, 40), (128256, 32), (2, 600)):
+        for n in range(1, most + 1):
+            assert verify(L, batch(seqs=1), vocab=vocab, ts=vocab, ds=vocab, target=1 << 40, draft=1 << 41, out=1 << 40,
+                          n=n, ws=1 << 42, nws=size(vocab, most, 1)) == E.DC_ERR_INVALID_ARG, (vocab, most, n)
+
+
 # ------------------------------------------------------------ page tables
 def table(**kw):
     return make(_lib.dc_kv_table, dict(seqs=4, width=10, page=16, num_pages=100, pages=0x1000, kv_len=0x2000, refs=0x3000), kw)
