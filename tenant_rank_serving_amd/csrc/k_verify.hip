@@ -22,6 +22,9 @@ namespace {
 
 constexpr int kThreads = kVerifyThreads, kVec = kVerifyVec;
 constexpr float kMinusInf = -__builtin_inff();
+// What sums over max(p - q, 0) may be from rounding alone where p = q: p and q are
+// good to 5e-14 each; ten times that counts as nothing.
+constexpr double kNothing = 0x1p-40;
 
 // s f + c with the constant in scalar registers: left to itself the compiler takes
 // the accumulating form and moves each constant to vector registers first, two
@@ -424,7 +427,8 @@ __global__ void __launch_bounds__(THREADS) k_verify_pick(VerifyArgs a) {
     for (int b = lane + 64; b < pieces; b += 64) all += sum_of(b, false);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) all += shfl_xor(all, x);
-    const bool all_p = !(all > 0.0);   // nothing left of p - q: p itself, whose sum is 1
+    // nothing left of p - q: p itself, whose sum is 1
+    const bool all_p = !(all > (minus ? kNothing : 0.0));
     const double aim = (double)r * (all_p ? 1.0 : all);
     double run = 0.0, before = 0.0;
     int piece = -1, spare = 0;

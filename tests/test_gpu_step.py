@@ -202,6 +202,53 @@ def test_verify_looked_up_drafts_of_likely_tokens(b, vocab, dtype):
     assert (out[alone] == at[4::5]).all() and (np.delete(out[rows], np.s_[4::5]) != np.delete(at, np.s_[4::5])).all()
 
 
+@pytest.mark.parametrize("vocab,dtype,pad,shift", [(5003, "f32", 3, 0.0), (5003, "bf16", 1, 0.0), (40, "f32", 1, 4.0), (12001, "f32", 0, 4.0),
+                                                   (70001, "bf16", 8, 0.0), (70001, "f32", 5, 4.0)])
+def test_verify_draft_distribution_equal_to_the_target(vocab, dtype, pad, shift):
+    """Equal distributions whose sums round differently (rows that lie differently, logits a constant apart): nothing is
+    left of p - q, and where a draft falls all the same p is drawn from."""
+    t = torch()
+    note("verify, p = q", vocab, dtype, pad, shift)
+    b = 32
+    v = Verify(vocab, [2] * b, vocab, dtype, True, "hot")
+    v.x = np.round(v.x * 16) / 16                            # so that the constant is added exactly
+    v.x[:, 5] = -np.inf
+    if dtype == "bf16":
+        v.x = vals(bits(v.x))
+    v.y = v.x + shift
+    rows = v.q_start[:-1]
+    v.tokens[rows + 1] = np.resize([-1, 5, vocab], b)        # outside the vocabulary, and one that neither allows
+    v.upload()
+    y = v.y.copy()
+    wide = np.full((v.n, vocab + pad), np.nan)
+    wide[:, :vocab] = y
+    v.dr = (dev_bits(bits(wide)) if dtype == "bf16" else dev_f32(wide))[:, :vocab]
+    v.run()
+    t.cuda.synchronize()
+    v.compare()
+
+
+@pytest.mark.parametrize("eps", [1e-1, 1e-3, 1e-5])
+def test_verify_draft_distribution_close_to_the_target(eps):
+    """Draft logits that differ from the target's by little: what is left of p - q is small beside p, whose rounding
+    (1e-13 of its sum) moves the borders by more of it."""
+    note("verify, close", eps)
+    b, vocab = 48, 701
+    v = Verify(14, [2] * b, vocab, "f32", True, "hot")
+    v.y = (v.x + np.random.default_rng(3).normal(size=v.x.shape) * eps).astype(np.float32).astype(np.float64)
+    v.accept[:] = np.nan                                     # no draft stands
+    v.upload()
+    v.run()
+    torch().cuda.synchronize()
+    out = v.out.cpu().numpy().reshape(b, 2)
+    for i in range(b):
+        p, q = (step.distribution(a[2 * i], v.temp[i]) for a in (v.x, v.y))
+        left = np.maximum(p - q, 0.0)
+        token, margin = step.pick(left, v.pick[i])
+        assert margin * left.sum() > 1e-12                   # ten times the rounding
+        assert out[i].tolist() == [token, -1], i
+
+
 def test_verify_greedy_ties_and_masks():
     note("verify, greedy")
     v = Verify(4, [3] * 6, 9001, "f32", True, "hot")
