@@ -129,7 +129,7 @@ __device__ __forceinline__ void keep_larger(float& m, int& at, float m2, int at2
 template <bool F32, int U>
 __global__ void __launch_bounds__(kThreads) k_verify_stats(VerifyArgs a) {
   __shared__ float sm[4];
-  __shared__ int sat[4], scount[4];
+  __shared__ int sat[4], scount[8];
   __shared__ double sz[4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int sides = a.q ? 2 : 1, c = blockIdx.x % a.chunks, rs = blockIdx.x / a.chunks, side = rs % sides, row = rs / sides;
@@ -138,24 +138,25 @@ __global__ void __launch_bounds__(kThreads) k_verify_stats(VerifyArgs a) {
   const int V = a.vocab;
   const void* l = side ? row_of<F32>(a.q, a.qs, row) : row_of<F32>(a.p, a.ps, row);
   const int lead = lead_of<F32>(l);
-  // the row's sequence: how many sequences end at or before it
-  int before = 0, first = 0;
-  for (int i = tid; i <= a.seqs; i += kThreads) {
-    const int s = a.q_start[i];
-    before += i > 0 && s <= row;
-    if (i == 0) first = s;
+  // The row's sequence: how many sequences end at or before it, by 256 of the starts
+  // at a time, evenly spaced among those in question.  (All of them in every block are
+  // the square of a batch: the statistics of 2^18 sequences of a row of 64 logits took
+  // 18.6 ms that way, 1.6 this way.)
+  const int first = a.q_start[0];
+  int seq = 0;   // so many do, and perhaps some of the next `open`
+  for (int open = a.seqs, turn = 0; open > 0; turn ^= 4) {
+    const int step = (open + kThreads - 1) / kThreads, at = (tid + 1) * step;
+    const uint64_t ends = __ballot(at <= open && a.q_start[seq + at] <= row);
+    if (lane == 0) scount[turn + wave] = __builtin_popcountll(ends);
+    __syncthreads();
+    const int n = (scount[turn] + scount[turn + 1] + scount[turn + 2] + scount[turn + 3]) * step;
+    seq += n;
+    open = min(open - n, step - 1);
   }
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) before += __shfl_xor(before, m);
-  if (lane == 0) scount[wave] = before;
-  if (tid == 0) sat[0] = first;
-  __syncthreads();
-  const int seq = scount[0] + scount[1] + scount[2] + scount[3];
-  if (seq >= a.seqs || row < sat[0]) return;   // a row of no sequence
+  if (seq >= a.seqs || row < first) return;   // a row of no sequence
   if (side && row + 1 >= a.q_start[seq + 1]) return;   // behind the last draft
   const double k = factor(a.temperature, seq);
   if (side && k == 0.0) return;
-  __syncthreads();
 
   float v[U][kVec];
   const int v0 = c * U * kThreads + tid;

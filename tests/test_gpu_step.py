@@ -341,6 +341,61 @@ def test_verify_captured_two_sizes_share_a_workspace():
         b.compare()
 
 
+@pytest.mark.parametrize("b", [255, 256, 257, 511, 513, 5000, 65535, 65537])
+def test_verify_many_sequences(b):
+    """Sequences in numbers around those whose starts a block looks at at once, empty ones among them."""
+    t = torch()
+    note("verify, many sequences", b)
+    rng = np.random.default_rng(b)
+    nq = rng.integers(0, 3, b)
+    nq[:2], nq[-2:] = 0, rng.integers(0, 2, 2)
+    vocab, q_start = 3, 4 + np.concatenate([[0], np.cumsum(nq)])
+    n = int(q_start[-1]) + 5
+    x = vals(bits(rng.normal(size=(n, vocab)) * 3))
+    picks, accept = rng.random(b).astype(np.float32), rng.random(n).astype(np.float32)
+    tokens, temp = rng.integers(0, vocab, n), np.resize([0.5, 1.0, 0.0, 2.0], b)
+    batch = trs.VerifyBatch(dev_i32(q_start), dev_i32(tokens), dev_f32(accept), dev_f32(picks), dev_f32(temp))
+    out, count = t.full((n,), -7, dtype=t.int32, device="cuda"), t.full((b,), -7, dtype=t.int32, device="cuda")
+    ws = t.full((trs.dc_verify_workspace_bytes(vocab, n, b),), 0xA5, dtype=t.uint8, device="cuda")
+    trs.dc_verify_drafts(batch, dev_bits(bits(x)), None, out, count, ws)
+    want, _, wcount, margin = step.verify(x, None, q_start, tokens, accept, picks, temp)
+    assert margin > 1e-11
+    assert count.tolist() == wcount and out.tolist() == [-7 if o is None else o for o in want]
+
+
+def shortest(call, before=lambda: None, times=5):
+    """The shortest of some calls, us."""
+    t = torch()
+    best = float("inf")
+    for _ in range(times):
+        before()
+        a, b = (t.cuda.Event(enable_timing=True) for _ in range(2))
+        t.cuda.synchronize()
+        a.record()
+        call()
+        b.record()
+        t.cuda.synchronize()
+        best = min(best, 1e3 * a.elapsed_time(b))
+    return best
+
+
+def test_verify_work_grows_with_the_batch_not_with_its_square():
+    """Four times as many sequences take about four times as long (10 times, where every row looks through all starts)."""
+    t = torch()
+    vocab, us = 8, []
+    for n in (1 << 17, 1 << 19):
+        note("verify, large batch", n, vocab)
+        x = t.randn(n, vocab, device="cuda").bfloat16()
+        batch = trs.VerifyBatch(t.arange(n + 1, dtype=t.int32, device="cuda"), t.zeros(n, dtype=t.int32, device="cuda"),
+                                t.rand(n, device="cuda"), t.rand(n, device="cuda"))
+        out, count = t.zeros(n, dtype=t.int32, device="cuda"), t.zeros(n, dtype=t.int32, device="cuda")
+        ws = t.empty(trs.dc_verify_workspace_bytes(vocab, n, n), dtype=t.uint8, device="cuda")
+        us.append(shortest(lambda: trs.dc_verify_drafts(batch, x, None, out, count, ws)))
+        assert (count == 1).all()
+    print("%.0f and %.0f us" % tuple(us))
+    assert us[1] < 6 * us[0]
+
+
 def test_verify_more_blocks_than_31_bits_of_threads():
     """Rows whose statistics take more than 2^31 threads: the counters that they clear on the way are those of the
     sequences, whatever a block's number."""
