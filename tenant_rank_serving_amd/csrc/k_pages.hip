@@ -82,10 +82,11 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
   __shared__ int box[kWaves];
   __shared__ uint32_t status;
   __shared__ int giving;   // sequences that give pages back, 64 for one with 64
+  __shared__ int part;     // the sequence that was dealt a part of what it needs
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int most = t.width * t.page, shift = 31 - __builtin_clz(t.page);
   auto pages_of = [&](int n) { return (int)(((int64_t)n + t.page - 1) >> shift); };
-  if (tid == 0) status = 0, giving = 0;
+  if (tid == 0) status = 0, giving = 0, part = -1;
   __syncthreads();
 
   // the first kResizeThreads sequences' lengths, in the order in which the waves
@@ -264,25 +265,9 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
     if (old < 0 || old > most || want < 0 || want > most) continue;
     const int end = (int)(upto[b] >> 1), first = b ? (int)(upto[b - 1] >> 1) : 0;
     const bool swap = upto[b] & 1;
-    if (end > first && end > have) {   // too few: what it was dealt goes back
+    if (end > first && end > have) {   // too few
       atomicOr(&status, (uint32_t)DC_KV_FULL);
-      int32_t* row = t.pages + (int64_t)b * t.width;
-      for (int k = first; k < have; ++k) {
-        const int slot = k - first;
-        if (swap && slot == 0) {
-          if (b0 == 0) {
-            t.refs[given[tid]] = 0;
-          } else {
-            t.refs[copies[2 * b + 1]] = 0;
-            row[old >> shift] = copies[2 * b];
-            copies[2 * b] = copies[2 * b + 1] = -1;
-          }
-        } else {
-          int32_t* e = row + pages_of(old) + slot - swap;
-          t.refs[*e] = 0;
-          *e = -1;
-        }
-      }
+      if (first < have) part = b;
       continue;
     }
     if (swap) {
@@ -296,6 +281,28 @@ __global__ void __launch_bounds__(kResizeThreads) k_resize(TableArgs t, const in
     t.kv_len[b] = want;
   }
   __syncthreads();
+  // What the one sequence was dealt that got some and not all goes back, by all
+  // threads (8000 pages 4 us; by one, which waits for each entry, 1150).
+  if (part >= 0) {
+    const int b = part, first = b ? (int)(upto[b - 1] >> 1) : 0, old = old_of[b];
+    const bool swap = upto[b] & 1;
+    int32_t* row = t.pages + (int64_t)b * t.width;
+    for (int slot = tid; slot < have - first; slot += kResizeThreads) {
+      if (swap && slot == 0) {
+        if (b < kResizeThreads) {
+          t.refs[given[b]] = 0;
+        } else {
+          t.refs[copies[2 * b + 1]] = 0;
+          row[old >> shift] = copies[2 * b];
+          copies[2 * b] = copies[2 * b + 1] = -1;
+        }
+      } else {
+        int32_t* e = row + pages_of(old) + slot - swap;
+        t.refs[*e] = 0;
+        *e = -1;
+      }
+    }
+  }
   if (tid == 0 && status) atomicOr(t.status, status);
 }
 

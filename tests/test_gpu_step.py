@@ -588,6 +588,55 @@ def test_tables_many_sequences():
     a.resize(rng.integers(0, 49, 16384))
 
 
+@pytest.mark.parametrize("at", [0, 700, 1500])
+@pytest.mark.parametrize("shared", [False, True])
+def test_tables_give_back_a_large_part(at, shared):
+    """A pool that runs out behind thousands of a sequence's pages, among the first 1024 sequences and behind them, with
+    and without an exchange of its last page: all of them are free again, and another sequence takes them."""
+    note("tables, a large part", at, shared)
+    seqs, width, page = 1600, 5000, 16
+    rng = np.random.default_rng(at)
+    pages, lens = np.full((seqs, width), -1, np.int32), np.zeros(seqs, np.int32)
+    refs = np.where(rng.random(9001) < 0.5, 0, 1).astype(np.int32)
+    held = np.nonzero(refs)[0]
+    pages[at, :2], lens[at] = held[:2], 20                   # a partly filled last page
+    if shared:
+        pages[at + 1, :2], lens[at + 1] = held[:2], 20
+        refs[held[:2]] = 2
+    t = Table(pages, lens, refs, page)
+    new = lens.copy()
+    new[at] = width * page                                   # 4998 or 4999 of about 4500 free ones
+    new[at + 3] = 40                                         # behind it: gets none
+    t.resize(new)
+    assert t.status.item() == trs.DC_KV_FULL and t.lens.tolist() == lens.tolist()
+    new[at] = lens[at]
+    t.status.zero_()
+    t.ref.full = False
+    new[at + 2], new[at + 3] = 4000 * page, 0
+    t.resize(new)
+    assert t.status.item() == 0 and t.lens[at + 2].item() == 4000 * page
+
+
+def test_tables_giving_back_a_part_takes_as_long_as_keeping_it():
+    t = torch()
+    note("tables, a part's time")
+    us = []
+    for num in (8192, 8000):
+        pages, lens = t.full((1, 8192), -1, dtype=t.int32, device="cuda"), t.zeros(1, dtype=t.int32, device="cuda")
+        refs, copies = t.zeros(num, dtype=t.int32, device="cuda"), t.zeros(1, 2, dtype=t.int32, device="cuda")
+        table, new, status = trs.KvTable(pages, lens, refs, 16), dev_i32([8192 * 16]), t.zeros(1, dtype=t.int32, device="cuda")
+
+        def empty():
+            pages.fill_(-1)
+            for x in (lens, refs, status):
+                x.zero_()
+
+        us.append(shortest(lambda: trs.dc_kv_resize(table, new, copies, status), empty))
+        assert status.item() == (trs.DC_KV_FULL if num < 8192 else 0) and bool((refs == (num == 8192)).all())
+    print("%.1f and %.1f us" % tuple(us))
+    assert us[1] < 10 * us[0]
+
+
 def test_tables_of_nearly_2_to_the_31_pages():
     """The most pages that 31 bits number, all held but a few at either end: what is read ahead ends with the counts."""
     t = torch()
