@@ -971,8 +971,9 @@ size_t dc_mx4_bytes(int32_t rows, int32_t cols);
 dc_status dc_mx4_pack_device(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, void* dst, size_t dst_bytes,
                              uint32_t* flag, void* stream);
 
-/* dc_mx4_dequant -- what a matrix in the format stands for, exactly: X device
- * bf16 [rows][cols], rows `stride` elements apart (a multiple of 8). */
+/* dc_mx4_dequant -- what a matrix in the format stands for, exactly (2^128 and
+ * more, which scales of 253 and 254 can be, is infinity in bf16): X device bf16
+ * [rows][cols], rows `stride` elements apart (a multiple of 8). */
 dc_status dc_mx4_dequant(const dc_mx4_view* w, uint16_t* X, int64_t stride, void* stream);
 
 /*

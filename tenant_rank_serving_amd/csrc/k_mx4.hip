@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(64 * NW, NW / 4) k_mx4(Mx4Args a) {
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint64_t large = 0;
   for (int g = wave; g < gc; g += NW) {
     const int H = g >> 2, j8 = 8 * (g & 3);
     uint4 w[RT];
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(64 * NW, NW / 4) k_mx4(Mx4Args a) {
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const float f = scale_of(s[r]);
+        const float f = scale_unless_large(s[r], &large);
         const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -184,6 +185,9 @@ __global__ void __launch_bounds__(64 * NW, NW / 4) k_mx4(Mx4Args a) {
         }
       }
     }
+  }
+  if constexpr (!XQ) {
+    if (large) add_large<RT, TT>(a, acc, r0, 16 * t0, wave, NW);
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r)

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(64 * WR * WK) k_mx4_few(Mx4Args g) {
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) load(s, s);
   int b = 0;
+  uint64_t large = 0;
   for (int s = 0; s < steps; ++s) {
     wait_barrier<(NS - 2) * L>();   // this step's tiles are here, the last one's have been read
     load(s + NS - 1, b == 0 ? NS - 1 : b - 1);
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(64 * WR * WK) k_mx4_few(Mx4Args g) {
       for (int r = 0; r < RT; ++r) {
         const uint4 w = *reinterpret_cast<const uint4*>(sh.l.w[b][wk][wr] + r * 1024 + lane * 16);
         const uint32_t sc = *reinterpret_cast<const uint32_t*>(sh.l.s[b][wk][wr] + r * 256 + lane * 4);
-        const float f = scale_of(sc >> (8 * (c & 3)) & 255u);
+        const float f = scale_unless_large(sc >> (8 * (c & 3)) & 255u, &large);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(64 * WR * WK) k_mx4_few(Mx4Args g) {
     }
     b = b + 1 == NS ? 0 : b + 1;
   }
+  if (large) add_large<RT, TT>(g, acc, wrow, t0, wk, WK);
   wait_barrier<0>();   // nothing is on its way to LDS, and everyone has left it
 
   if constexpr (WK > 1) {

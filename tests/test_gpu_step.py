@@ -1035,6 +1035,44 @@ def test_mx4_scales_at_their_ends(low):
     assert (np.abs(vals(host_bits(y)) - want) <= mx4_tolerance(w, x4, want)).all()
 
 
+@pytest.mark.parametrize("t_", [1, 9, 16, 17, 40, 100, 300, 520])
+@pytest.mark.parametrize("least", [250, 253])
+def test_mx4_numbers_larger_than_bf16_holds(t_, least):
+    """Scales up to the last one, 254: the products are those of the formula where the numbers themselves pass bf16's
+    largest, among small ones, blocks without a number and one that is NaN."""
+    t = torch()
+    note("mx4, large scales", t_, least)
+    rng = np.random.default_rng(t_ + least)
+    out, inn = 1152, 640
+    codes = rng.integers(0, 16, (out, inn))
+    scale = rng.integers(least, 255, (out, inn // 32))
+    scale[rng.random(scale.shape) < 0.1] = 128
+    codes.reshape(out, -1, 32)[rng.random(scale.shape) < 0.1] = 0
+    scale[7, 3] = 255
+    view = trs.Mx4View(out, inn, t.from_numpy(step.mx4_pack(codes, scale)).cuda())
+    w = step.mx4_matrix(codes, scale)
+    x = vals(bits(rng.normal(size=(t_, inn)) * 2.0 ** -100))
+    y = t.zeros(t_, out, dtype=t.bfloat16, device="cuda")
+    xq = mx4_empty(t_, inn)
+    trs.dc_mx4_pack_device(dev_bits(bits(x)), xq)
+    x4 = step.mx4_matrix(*step.mx4_quantize(x))
+    for xs, call, arg in ((x, trs.dc_apply_mx4, dev_bits(bits(x))), (x4, trs.dc_apply_mx4q, xq)):
+        call(view, arg, y)
+        got = vals(host_bits(y))
+        assert np.isnan(got[:, 7]).all()
+        got[:, 7] = 0.0
+        w0 = np.nan_to_num(w)
+        w0[7] = 0.0
+        want = xs @ w0.T
+        # four products at a quarter for one: five times the sums' roundings at most
+        tol = BF16 * np.abs(want) + 5 * (inn * 1.125 + 8) * 2.0 ** -23 * (np.abs(xs) @ np.abs(w0).T)
+        assert (np.abs(got - want) <= tol).all()
+    back = t.zeros(out, inn, dtype=t.bfloat16, device="cuda")
+    trs.dc_mx4_dequant(view, back)
+    want = np.where(np.abs(w) >= 2.0 ** 128, np.copysign(np.inf, w), w)
+    assert np.array_equal(vals(host_bits(back)), want, equal_nan=True)
+
+
 def test_mx4_captured():
     t = torch()
     note("mx4, captured")
