@@ -219,15 +219,19 @@ void go(const Mx4Args& a) {
 // tokens: 4096 x 4096 16 rows 3.4 / 4.4 / 5.9, 48 rows 4.7 / 5.3 / 6.8; 11008 x 4096
 // 16 rows 5.7 / 8.9 / 13.4, 48 rows 4.8 / 5.5 / 7.2; 32000 x 4096 32 rows 11.9 / 12.7
 // / 18.6, 64 rows 13.1 / 13.3 / 15.5.
-int launch_mx4(const Mx4Args& a) {
-  if (a.T > 16) return launch_mx4_few(a);
+int mx4_row_tiles(int32_t out, int32_t T) {
   int best = 1;
   int64_t least = INT64_MAX;
   for (int rt = 1; rt <= 4; ++rt) {
-    const int64_t cost = ((a.out / 16 + rt - 1) / rt + 255) / 256 * (17 * rt + 4 * a.T);
+    const int64_t cost = ((out / 16 + rt - 1) / rt + 255) / 256 * (17 * rt + 4 * T);
     if (cost < least) least = cost, best = rt;
   }
-  switch (best) {
+  return best;
+}
+
+int launch_mx4(const Mx4Args& a) {
+  if (a.T > 16) return launch_mx4_few(a);
+  switch (mx4_row_tiles(a.out, a.T)) {
     case 1: go<1, 1, false>(a); break;
     case 2: go<2, 1, false>(a); break;
     case 3: go<3, 1, false>(a); break;
@@ -247,7 +251,7 @@ int launch_mx4(const Mx4Args& a) {
 //   and 256x256: 4096 x 4096 2048 tokens 21.6 and 30.5, 4096 42.3 and 40.2, 8192
 //   84.9 and 78.7; 11008 x 4096 2048 tokens 57 and 62, 4096 118 and 108, 8192 219
 //   and 212; 32000 x 4096, 8192 tokens 588 and 516
-int launch_mx4q(const Mx4Args& a) {
+int mx4q_tile(int32_t out, int32_t in, int32_t T) {
   constexpr struct {
     int rows, toks, first, end, step;
   } kTiles[] = {{16, 16, 2200, 0, 32}, {16, 32, 2300, 0, 35},    {32, 32, 2100, 0, 48},      {32, 64, 2600, 0, 70},
@@ -255,10 +259,15 @@ int launch_mx4q(const Mx4Args& a) {
   int best = 0;
   int64_t least = INT64_MAX;
   for (int c = 0; c < 8; ++c) {
-    const int64_t tiles = (int64_t)((a.out + kTiles[c].rows - 1) / kTiles[c].rows) * ((a.T + kTiles[c].toks - 1) / kTiles[c].toks);
-    const int64_t cost = kTiles[c].first + (tiles + 255) / 256 * (kTiles[c].end + (int64_t)kTiles[c].step * (a.in / 128));
+    const int64_t tiles = (int64_t)((out + kTiles[c].rows - 1) / kTiles[c].rows) * ((T + kTiles[c].toks - 1) / kTiles[c].toks);
+    const int64_t cost = kTiles[c].first + (tiles + 255) / 256 * (kTiles[c].end + (int64_t)kTiles[c].step * (in / 128));
     if (cost < least) least = cost, best = c;
   }
+  return best;
+}
+
+int launch_mx4q(const Mx4Args& a) {
+  const int best = mx4q_tile(a.out, a.in, a.T);
   switch (best) {
     case 0: go<1, 1, true>(a); break;
     case 1: go<1, 2, true>(a); break;

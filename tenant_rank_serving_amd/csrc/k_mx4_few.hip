@@ -173,20 +173,24 @@ void go(const Mx4Args& a) {
 // 64 tokens 32x32 7.5, 32x16 8.1, 64x32 of 8 waves 8.6; 128 tokens 8.9 of 8 waves,
 // 11.0 of 4; 256 tokens 16.5 and 13.4, 128x64 18.6; 512 tokens 64x32 24.9, 128x64
 // 19.6; 11008 x 4096, 32 tokens 64x32 of 8 waves 9.4, of 4 11.0, 32x16 11.3
-int launch_mx4_few(const Mx4Args& a) {
+int mx4_few_tile(int32_t out, int32_t in, int32_t T) {
   constexpr struct {
     int rows, toks, first, step, least;   // least: hundredths of a block
   } kTiles[] = {{32, 16, 2200, 88, 100}, {32, 32, 1500, 183, 100}, {64, 32, 1500, 235, 100}, {64, 32, 1500, 186, 155}, {128, 64, 1000, 540, 100}};
   int best = 0;
   int64_t least = INT64_MAX;
   for (int c = 0; c < 5; ++c) {
-    const int64_t blocks = (int64_t)((a.out + kTiles[c].rows - 1) / kTiles[c].rows) * ((a.T + kTiles[c].toks - 1) / kTiles[c].toks);
+    const int64_t blocks = (int64_t)((out + kTiles[c].rows - 1) / kTiles[c].rows) * ((T + kTiles[c].toks - 1) / kTiles[c].toks);
     int64_t n = (blocks + 255) / 256 * 100;
     if (n < kTiles[c].least) n = kTiles[c].least;
-    const int64_t cost = kTiles[c].first + n * kTiles[c].step * (a.in / 128) / 100;
+    const int64_t cost = kTiles[c].first + n * kTiles[c].step * (in / 128) / 100;
     if (cost < least) least = cost, best = c;
   }
-  switch (best) {
+  return best;
+}
+
+int launch_mx4_few(const Mx4Args& a) {
+  switch (mx4_few_tile(a.out, a.in, a.T)) {
     case 0: go<1, 1, 2, 4, 3>(a); break;
     case 1: go<1, 2, 2, 4, 3>(a); break;
     case 2: go<2, 2, 2, 4, 2>(a); break;

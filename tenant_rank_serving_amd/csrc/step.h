@@ -78,6 +78,11 @@ inline size_t mx4_codes(int32_t rows, int32_t cols) { return ((size_t)rows + 15)
 int launch_mx4(const Mx4Args& a);
 int launch_mx4_few(const Mx4Args& a);   // of it, more than 16 tokens
 int launch_mx4q(const Mx4Args& a);
+// Which form a call takes: row tiles of 16 rows of a block (up to 16 tokens), and
+// numbers in the lists of tiles of the other two.  Tests look at them.
+int mx4_row_tiles(int32_t out, int32_t T);
+int mx4_few_tile(int32_t out, int32_t in, int32_t T);
+int mx4q_tile(int32_t out, int32_t in, int32_t T);
 int launch_mx4_tiles(const Mx4Args& a, int32_t size);   // of it, by tiles in LDS: 64 x 64, 64 x 128, 128 x 128, 256 x 256
 int launch_mx4_pack(int32_t rows, int32_t cols, const uint16_t* X, int64_t stride, uint8_t* dst, uint32_t* flag,
                     void* stream);

@@ -975,6 +975,56 @@ def test_apply_mx4q_tiles(t_, out, inn):
     assert t.equal(y[:t_], first[:t_])
 
 
+# The form that a call takes (csrc/step.h), and calls of each: tokens that end inside
+# a tile, columns of 1, 2, 3 and 0 more than whole groups of 512.
+MX4_FORMS = ["%d x 16" % (16 * r) for r in (1, 2, 3, 4)] + ["few " + x for x in ("32 x 16", "32 x 32", "64 x 32 of 8 waves", "64 x 32", "128 x 64")]
+MX4Q_FORMS = ["16 x 16", "16 x 32", "32 x 32", "32 x 64", "64 x 64", "64 x 128", "128 x 128", "256 x 256"]
+
+
+def mx4_form(t_, out, inn):
+    L = trs.lib()
+    return MX4_FORMS[L._ZN2dc13mx4_row_tilesEii(out, t_) - 1 if t_ <= 16 else 4 + L._ZN2dc12mx4_few_tileEiii(out, inn, t_)]
+
+
+def mx4q_form(t_, out, inn):
+    return MX4Q_FORMS[trs.lib()._ZN2dc9mx4q_tileEiii(out, inn, t_)]
+
+
+MX4_CALLS = {
+    "16 x 16": [(5, 1152, 512), (15, 128, 640), (2, 1152, 256), (9, 128, 384)],
+    "32 x 16": [(1, 4224, 512), (5, 4224, 640), (9, 4224, 256), (15, 6272, 384)],
+    "48 x 16": [(2, 8320, 512), (5, 8320, 640), (9, 8320, 256), (15, 11008, 384)],
+    "64 x 16": [(1, 12416, 512), (5, 12416, 640), (9, 12416, 256), (15, 32000, 384)],
+    "few 32 x 16": [(17, 128, 1024), (17, 128, 1152), (19, 1152, 1792), (17, 128, 1408)],
+    "few 32 x 32": [(17, 128, 512), (50, 1152, 640), (61, 1152, 256), (17, 128, 384)],
+    "few 64 x 32 of 8 waves": [(33, 4224, 512), (33, 4224, 640), (50, 4224, 256), (33, 4224, 384)],
+    "few 64 x 32": [(33, 11008, 512), (33, 11008, 640), (33, 11008, 768), (33, 11008, 384)],
+    "few 128 x 64": [(65, 11008, 512), (17, 128, 128), (33, 11008, 256), (65, 11008, 384)],
+}
+MX4Q_CALLS = {
+    "16 x 16": [(17, 128, 1024), (17, 128, 1152), (15, 384, 1280), (17, 128, 896)],
+    "16 x 32": [(50, 1152, 2560), (61, 1152, 2176), (19, 2176, 2304), (33, 2048, 2432)],
+    "32 x 32": [(17, 128, 512), (50, 1152, 640), (61, 1152, 256), (17, 128, 384)],
+    "32 x 64": [(100, 11008, 1024), (33, 32000, 640), (33, 32000, 768), (100, 6400, 1408)],
+    "64 x 64": [(33, 32000, 1024), (100, 6400, 1664), (700, 11008, 256), (33, 32000, 896)],
+    "64 x 128": [(4100, 384, 1024), (65, 11008, 2176), (1100, 6400, 256), (4100, 384, 896)],
+    "128 x 128": [(65, 32000, 512), (65, 32000, 640), (65, 32000, 768), (100, 32000, 384)],
+    "256 x 256": [(5300, 5888, 1408), (4500, 10496, 1280), (5800, 7936, 1536), (1100, 11136, 1664)],
+}
+
+
+@pytest.mark.parametrize("form,t_,out,inn", [(f, *c) for f, cs in MX4_CALLS.items() for c in cs])
+def test_apply_mx4_forms(form, t_, out, inn):
+    assert mx4_form(t_, out, inn) == form
+    test_apply_mx4_tiles(t_, out, inn)
+
+
+@pytest.mark.parametrize("form,t_,out,inn", [(f, *c) for f, cs in MX4Q_CALLS.items() for c in cs])
+def test_apply_mx4q_forms(form, t_, out, inn):
+    assert mx4q_form(t_, out, inn) == form
+    test_apply_mx4q_tiles(t_, out, inn)
+
+
 # The largest tile: two or three for a block, columns of whole groups of 512 and of 1, 2 and 3 more.
 @pytest.mark.parametrize("t_,out,inn", [(5300, 5888, 1408), (4500, 10496, 1280), (5800, 7936, 1536), (6300, 6912, 1664), (4600, 6272, 2048)])
 def test_apply_mx4q_largest_tiles(t_, out, inn):

@@ -272,6 +272,20 @@ def test_mx4_bytes_at_the_ends_of_its_arguments(L):
     assert pack(L, rows=1, cols=cols, stride=cols, x=1 << 40, dst=1 << 44, n=trs.dc_mx4_bytes(1, cols) - 1) == E.DC_ERR_BUFFER
 
 
+def test_mx4_forms_that_the_gpu_tests_name():
+    """Every form of the products has its calls in the GPU tests, whatever the rules become: whole and ragged columns, tokens
+    that end inside a tile."""
+    import test_gpu_step as g
+    for forms, calls, of, tokens in ((g.MX4_FORMS, g.MX4_CALLS, g.mx4_form, lambda f: 16 if f in g.MX4_FORMS[:4] else int(f.split()[3])),
+                                     (g.MX4Q_FORMS, g.MX4Q_CALLS, g.mx4q_form, lambda f: int(f.split()[2]))):
+        assert list(calls) == forms
+        for form, cases in calls.items():
+            for t, out, inn in cases:
+                assert of(t, out, inn) == form, (form, t, out, inn, of(t, out, inn))
+                assert t % tokens(form) and out % 128 == 0
+            assert {inn // 128 % 4 for _, _, inn in cases} == {0, 1, 2, 3}, form
+
+
 def test_mx4_refusals(L):
     assert apply(L) == E.DC_OK and pack(L, rows=0) == E.DC_OK and pack(L, rows=0, n=0, flag=None) == E.DC_OK
     size = trs.dc_mx4_bytes(256, 384)
