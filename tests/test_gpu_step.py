@@ -420,6 +420,24 @@ def test_verify_more_blocks_than_31_bits_of_threads():
     assert got[:, 0].tolist() == want[::2] and (got[:, 1:] == -1).all() and (count == 1).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_verify_rows_behind_32_bits(dtype):
+    """Rows whose offsets pass 2^32 elements."""
+    t = torch()
+    note("verify, far rows", dtype)
+    v = Verify(15, [3, 2, 4], 2500, dtype, True, "hot").upload()
+    stride = (1 << 29) + 16
+    far = []
+    for a in (v.target, v.dr):
+        room = t.empty(stride * (v.n - 1) + 2500, dtype=a.dtype, device="cuda").as_strided((v.n, 2500), (stride, 1))
+        far.append(room.copy_(a))
+    assert stride * (v.n - 1) >= 1 << 32
+    v.target, v.dr = far
+    v.run()
+    t.cuda.synchronize()
+    v.compare()
+
+
 def test_verify_binding_refusals():
     t = torch()
     v = Verify(12, [2, 2], 64, "f32", True).upload()
@@ -756,6 +774,36 @@ def test_compact(layers, heads, page, dim, kv, order, lens, share, inplace):
         for side in range(2):
             p.host[l, side] = step.compact(p.host[l, side], tables[0], start, keep, to, page)
     p.check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_pages_behind_32_bits(kv):
+    """Pages whose offsets pass 2^32 bytes and elements, keys and values of two layers in the room between each other's:
+    copied, and compacted to other pages and in place."""
+    t = torch()
+    note("pages, far", kv)
+    heads, page, dim, pages, layers, stride = 3, 16, 64, 18, 2, (1 << 28) + 8192
+    p = Layers(5, layers, pages, heads, page, dim, kv)
+    room = t.empty(stride * pages, dtype=p.dev.dtype, device="cuda")
+    size = heads * page * dim
+    shape, strides = (layers, 2, pages, heads, page, dim), (2 * size, size, stride, page * dim, dim, 1)
+    far = room.as_strided(shape, strides)
+    far.view(p.int).copy_(p.dev.view(p.int))
+    p.dev = far
+    p.layers = trs.KvLayers([trs.KvCache(x[0], x[1]) for x in far.unbind(0)])
+    assert stride * (pages - 1) > 1 << 32
+    trs.dc_kv_copy(p.layers, dev_i32([[17, 1], [2, 16], [15, 14]]))
+    for a, b in ((17, 1), (2, 16), (15, 14)):
+        p.host[:, :, b] = p.host[:, :, a]
+    p.check()
+    src, dst = np.array([[17, 0, 16], [3, 15, -1]], np.int32), np.array([[4, 13, -1], [12, 5, -1]], np.int32)
+    start, keep = np.array([0, 20, 29], np.int32), np.concatenate([np.arange(1, 41, 2), np.arange(0, 27, 3)]).astype(np.int32)
+    for to in (dst, None):
+        trs.dc_kv_compact(p.layers, dev_i32(src), dev_i32(start), dev_i32(keep), None if to is None else dev_i32(to))
+        for l in range(layers):
+            for side in range(2):
+                p.host[l, side] = step.compact(p.host[l, side], src, start, keep, src if to is None else to, page)
+        p.check()
 
 
 def test_compact_numbers_out_of_range():
