@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) k_mx4_dequant(const uint8_t* __restrict__
 
 // ---------------------------------------------------------------- products
 // Block: RT 16-row tiles of the matrix x TT 16-token tiles, all columns; NW
-// waves take the 512-column groups in turn and add their sums through LDS: one
+// waves take the 128-column groups in turn and add their sums through LDS: one
 // launch, no workspace.  Lane l holds row (token) l%16 and block l/16 of 128
 // columns; result: token l%16, rows 4(l/16) .. +4.
 // Bound by latency (4096 x 4096, 1 token: 3.4 us, of which the weights at HBM's rate

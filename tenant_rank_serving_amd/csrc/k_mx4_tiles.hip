@@ -20,10 +20,15 @@
 // 32000 x 4096 with 8192 tokens 548 and 516; and operands of two steps in registers
 // at once, 7 more than there are.)
 //
-// Measured, 16384 tokens x 11008 x 4096 (1.48 TFLOP), normal numbers: 355 to 375 us,
-// 4.0 PFLOP/s.  Bound by the power that the card may take: without writing results
-// 315, without loads 327, with operands that stay 290, products alone 214, at 1.6
-// GHz.  Not faster: results written over the next tile's steps instead of at once
+// Measured, 16384 tokens x 11008 x 4096 (1.48 TFLOP), normal numbers: 335 to 375 us,
+// 4.0 to 4.4 PFLOP/s.  Two things bound it.  A turn takes twice its products' cycles:
+// of 640000 cycles the matrix pipes are busy 352000; LDS serves reads for 149000
+// (no bank conflicts), and waves wait for it 11 % of their time, so it is not the
+// port that fills the rest but what a turn waits for in a row, loads, reads and two
+// barriers.  And the power that the card may take: with all codes zero the same
+// cycles run at 2.45 GHz and take 264 us, with normal numbers at 1.97.  Parts taken
+// away in a copy: results 315, loads 327, operands that stay 290; products alone, from
+// registers, 206 (zero codes 156).  Not faster: results written over the next tile's steps instead of at once
 // (361), products of 32 x 32 x 64 (365), wave tiles of 128 x 128 (the compiler moves
 // their sums about).  Results go out as 64 bytes a token, past the caches: 16-byte
 // pieces cost 10 % more, 32-byte pieces 70 %, cached stores 3 %.
@@ -56,8 +61,8 @@ struct TilesLds {
   alignas(256) uint8_t bs[TB * kBs];
 };
 
-// wait_barrier, or M more or as many loads as there are where `fresh`.  (The branch
-// is hidden from the compiler, which makes copies of the steps for either side.)
+// wait_barrier, and with no wait for loads where `fresh`.  (The branch is hidden from
+// the compiler, which makes copies of the steps for either side.)
 template <int N>
 __device__ __forceinline__ void wait_barrier_unless(int fresh) {
   asm volatile(
@@ -66,6 +71,7 @@ __device__ __forceinline__ void wait_barrier_unless(int fresh) {
       : "memory", "scc");
 }
 
+// wait_barrier, with M more on their way where `fresh`.
 template <int N, int M>
 __device__ __forceinline__ void wait_barrier_more(int fresh) {
   asm volatile(

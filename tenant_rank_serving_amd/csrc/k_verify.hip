@@ -272,7 +272,8 @@ __device__ __forceinline__ double lane64(double v, int l) {
 // for each other) and with many blocks by the vector unit, half of it for the
 // decision that each block repeats: 63 sequences of 9 rows of 100003 bf16 logits
 // take 35 us by pieces of 2048 logits, 29 by 4096, 44 by 8192 (blocks of 16 waves
-// leave CUs waiting for their slowest).
+// leave CUs waiting for their slowest).  Blocks of 16 waves are started 0.2 us apart
+// on an XCD, whatever they do: 2^20 sequences without rows take 25 ms.
 template <bool F32, bool Q, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_verify_pick(VerifyArgs a) {
   constexpr int WAVES = THREADS / 64;
