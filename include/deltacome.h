@@ -986,7 +986,7 @@ dc_status dc_mx4_dequant(const dc_mx4_view* w, uint16_t* X, int64_t stride, void
  * fp32 sums in a fixed order; must not overlap x nor W.  A NaN block, or an x
  * that is not finite, reaches its row and token only.
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_UNSUPPORTED
- * (2^31 entries of W or of x, or more than 1048560 tokens).
+ * (2^31 entries of W or of an x in the format, or more than 1048560 tokens).
  */
 dc_status dc_apply_mx4(const dc_mx4_view* w, const uint16_t* x, uint16_t* y, int32_t T, void* stream);
 dc_status dc_apply_mx4q(const dc_mx4_view* w, const dc_mx4_view* x, uint16_t* y, void* stream);

@@ -1079,6 +1079,36 @@ def test_apply_mx4q_largest_tiles(t_, out, inn):
     test_apply_mx4q_tiles(t_, out, inn)
 
 
+@pytest.mark.parametrize("t_,out,inn,four", [(530001, 128, 4096, False), (300001, 8064, 128, True), (270001, 8064, 128, False)])
+def test_mx4_rows_behind_32_bits(t_, out, inn, four):
+    """Activations of more than 2^31 entries, results that pass 2^32 bytes: rows at either end, around the borders and between."""
+    t = torch()
+    note("mx4, far rows", t_, out, inn, four)
+    rng = np.random.default_rng(out)
+    w, view = mx4_case(rng, out, inn)
+    g = t.Generator(device="cuda")
+    g.manual_seed(1)
+    x = t.randn(t_, inn, generator=g, device="cuda", dtype=t.bfloat16)
+    y = t.full((t_ + 1, out), float("nan"), dtype=t.bfloat16, device="cuda")
+    assert max(t_ * inn, t_ * out) > 1 << 31
+    if four:
+        xq = mx4_empty(t_, inn)
+        trs.dc_mx4_pack_device(x, xq)
+        trs.dc_apply_mx4q(view, xq, y[:t_])
+    else:
+        trs.dc_apply_mx4(view, x, y[:t_])
+    ends = [k * (1 << 31) // n for n in (inn, out) for k in (1, 2) if k * (1 << 31) // n < t_]
+    rows = np.unique(np.concatenate([np.arange(40), t_ - 1 - np.arange(300), *[e + np.arange(-40, 40) for e in ends], rng.integers(0, t_, 300)]))
+    rows = rows[(rows >= 0) & (rows < t_)]
+    at = t.from_numpy(rows).cuda()
+    xs = x[at].double().cpu().numpy()
+    if four:
+        xs = step.mx4_matrix(*step.mx4_quantize(xs))
+    want = xs @ w.T
+    assert (np.abs(y[at].double().cpu().numpy() - want) <= mx4_tolerance(w, xs, want)).all()
+    assert bool(y[t_].isnan().all()) and not any(bool(part.isnan().any()) for part in y[:t_].split(1 << 15))
+
+
 @pytest.mark.parametrize("t_", [1, 20, 70, 300])
 def test_mx4_values_that_are_not_finite(t_):
     """A NaN block reaches its row, an x that is not finite its token; neither reaches further."""
