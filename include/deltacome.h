@@ -813,11 +813,12 @@ dc_status dc_apply_w4(const dc_w4_view* w, const uint16_t* x, uint16_t* y, int32
  *                aligned; holds nothing between calls.  The size falls with none
  *                of the three: the largest call's workspace serves smaller ones
  * Arithmetic: weights, sums and comparisons in fp64 (the exponentials to 2e-14),
- * in a fixed order: the tokens are those of the formula wherever its two sides
- * differ by more than about 1e-13 of p's sum, 1.  (Where little is left of p - q,
- * that is more of what is left: the borders between tokens are then good to 1e-13
- * / sum max(p - q, 0) of it.)  max(p - q, 0) of a draft model's q counts as zero
- * everywhere if it sums to 2^-40 or less: rounding alone may leave up to 1e-13.
+ * in a fixed order.  A draft stands or falls as by the formula wherever its two
+ * sides differ by more than about 1e-13 of them; the new token is the formula's
+ * wherever pick[b] sum w is further than about 1e-13 of p's sum from a border
+ * between tokens (where little is left of p - q, that is more of what is left).
+ * max(p - q, 0) of a draft model's q counts as zero everywhere if it sums to 2^-40
+ * or less: rounding alone may leave 1e-13.
  * Errors: DC_ERR_INVALID_ARG, DC_ERR_SHAPE, DC_ERR_ALIGN, DC_ERR_BUFFER,
  * DC_ERR_UNSUPPORTED (a vocabulary of more than 2^30; 2^24 pieces of 8192
  * logits or more in the rows of target and draft, or 2^22 in one row of each
