@@ -28,9 +28,9 @@
 // barriers.  And the power that the card may take: with all codes zero the same
 // cycles run at 2.45 GHz and take 264 us, with normal numbers at 1.97.  Parts taken
 // away in a copy: results 315, loads 327, operands that stay 290; products alone, from
-// registers, 206 (zero codes 156)..  Not faster: results written over the next tile's
+// registers, 206 (zero codes 156).  Not faster: results written over the next tile's
 // steps instead of at once (361), products of 32 x 32 x 64 (365), wave tiles of 128 x
-// 128 (the compiler moves their sums about)..  Results go out as 64 bytes a token, past
+// 128 (the compiler moves their sums about).  Results go out as 64 bytes a token, past
 // the caches: 16-byte pieces cost 10 % more, 32-byte pieces 70 %, cached stores 3 %.
 #include <hip/hip_runtime.h>
 
